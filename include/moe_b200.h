@@ -92,6 +92,8 @@ extern "C" {
 #define MOE_BF16            1   /* bf16 activations and weights, fp32 accumulate */
 #define MOE_FP8_E4M3_BLOCK  2   /* e4m3 dispatch + weights with block scales,
                                    bf16 expert outputs and layer output          */
+#define MOE_MXFP4           3   /* MXFP4 operands (moe_mxfp4_*); the layer's entry
+                                   points reject it                              */
 
 /* Layer shape.  Mirrors the reference module's constructor
  * (d_model, n_routed, n_shared, top_k, d_ff) plus the batch size, the shared
@@ -294,6 +296,65 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
                       void* out, float* f, float* P, float* loss,
                       int32_t* topk_idx, float* gates, int32_t* counts,
                       void* ws, void* stream);
+
+/* ---- microscaled 4-bit floating point (MXFP4) -------------------------------
+ * A matrix in MXFP4 is dense row-major E2M1 codes (rows, cols/2), two per
+ * byte with the even column in the low nibble, and E8M0 scale bytes
+ * (rows, cols/32): a code stands for its E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 and their negatives) times 2^(scale - 127); scale 255 makes its block NaN.
+ *
+ * moe_mxfp4_quantize: the scale of a block is the smallest power of two 2^k,
+ * k >= -126, with amax <= 6 * 2^k (2^0 for a block of zeros); codes round to
+ * nearest even.  A block that holds an infinity or a NaN gets scale 255 and
+ * codes 0.  moe_mxfp4_dequantize writes the values (bf16: rounded to nearest
+ * even, which is exact unless the value leaves bf16's normal range).
+ *   x / out  (rows, cols) fp32 or bf16 (dtype MOE_F32 / MOE_BF16), 16-byte
+ *            aligned; codes 16-byte aligned; cols a multiple of 32.
+ * rows may be 0 (nothing is launched).  A stack of matrices is one matrix
+ * with all their rows. */
+MOE_EXPORT int moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t cols,
+                                  uint8_t* codes, uint8_t* scales, void* stream);
+MOE_EXPORT int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                                    void* out, int32_t dtype, void* stream);
+
+/* The grouped product of MXFP4 operands over caller-made segments (as
+ * moe_expert_ffn_segments lays them out): for every row r of segment i,
+ * seg_offsets[i] <= r < seg_offsets[i+1], and every column j < n,
+ *   y[r, j] = act(sum_k a[r, k] w[seg_mat[i], j, k] + bias[seg_mat[i], j])
+ * summed in fp32 on the tensor cores.  act: none, or z / (1 + e^-z).  y is
+ * fp32, bf16 (round to nearest even), or MXFP4 codes with y_scales, quantised
+ * as moe_mxfp4_quantize would the fp32 results: the next product's operand.
+ *   a (rows, k/2), a_scales (rows, k/32): 0 <= rows; k a multiple of 128
+ *   w (n_mats, n, k/2), w_scales (n_mats, n, k/32): n a multiple of 32
+ *   bias (n_mats, n) fp32 or NULL
+ *   seg_offsets (n_seg+1), seg_mat (n_seg) int32 device, 1 <= n_seg <= 256
+ *   y (rows, n); y_scales (rows, n/32) with MOE_MXFP4, else NULL
+ *   ws moe_mxfp4_workspace_size() bytes (the status word), 256-byte aligned,
+ *      zero-filled once by moe_mxfp4_workspace_init
+ * Rows outside every segment are not written.  A segment whose bounds lie
+ * outside [0, rows] or whose matrix is outside [0, n_mats) is skipped and sets
+ * MOE_DEV_BAD_ROUTING.  Pointers 16-byte aligned. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1
+typedef struct {
+    int32_t rows;        /* rows of a and y                       */
+    int32_t n;           /* columns of y (rows of a weight matrix) */
+    int32_t k;           /* columns of a                          */
+    int32_t n_mats;      /* weight matrices, 1..65535             */
+    int32_t n_seg;       /* segments                              */
+    int32_t activation;  /* MOE_ACT_*                             */
+    int32_t out_dtype;   /* MOE_F32 | MOE_BF16 | MOE_MXFP4        */
+} moe_mxfp4_shape;
+
+MOE_EXPORT int moe_mxfp4_workspace_size(const moe_mxfp4_shape* shape, size_t* bytes);
+MOE_EXPORT int moe_mxfp4_workspace_init(const moe_mxfp4_shape* shape, void* ws, void* stream);
+/* Synchronises `stream` and returns the status word, as moe_get_device_status. */
+MOE_EXPORT int moe_mxfp4_get_device_status(const moe_mxfp4_shape* shape, void* ws, void* stream,
+                                           int32_t* status, int32_t clear);
+MOE_EXPORT int moe_mxfp4_matmul(const moe_mxfp4_shape* shape, const uint8_t* a, const uint8_t* a_scales,
+                                const int32_t* seg_offsets, const int32_t* seg_mat,
+                                const uint8_t* w, const uint8_t* w_scales, const float* bias,
+                                void* y, uint8_t* y_scales, void* ws, void* stream);
 
 /* ---- self-test of the bounded-wait path ------------------------------------
  * Launches one block that waits on an mbarrier which nothing completes, with

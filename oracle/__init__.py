@@ -6,3 +6,4 @@ benchmark's CPU-baseline leg may import it; the product library never does,
 and the two share no code.
 """
 from .moe_oracle import *  # noqa: F401,F403
+from .mxfp4 import *  # noqa: F401,F403

@@ -28,7 +28,8 @@ MOE_ERR_BAD_ROUTING = 4
 MOE_ERR_DEVICE_TIMEOUT = 5
 MOE_DEV_BAD_ROUTING = 0x1
 MOE_DEV_TIMEOUT = 0x2
-MOE_F32, MOE_BF16, MOE_FP8_E4M3_BLOCK = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3_BLOCK, MOE_MXFP4 = 0, 1, 2, 3
+MOE_ACT_NONE, MOE_ACT_SILU = 0, 1
 MOE_BIAS_LOGITS, MOE_BIAS_SELECTION = 0, 1
 MOE_PRIORITY_TOKEN, MOE_PRIORITY_SLOT = 0, 1
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_PASS = 0, 1
@@ -38,7 +39,8 @@ EXPORTED = (
     "moe_last_cuda_error", "moe_status_string", "moe_route", "moe_dispatch", "moe_expert_ffn",
     "moe_combine", "moe_balance_stats", "moe_layer_forward", "moe_selftest_wait_timeout",
     "moe_dispatch_noalloc", "moe_kernel_launches", "moe_backward_workspace_size", "moe_layer_backward",
-    "moe_expert_ffn_segments",
+    "moe_expert_ffn_segments", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_workspace_size",
+    "moe_mxfp4_workspace_init", "moe_mxfp4_get_device_status", "moe_mxfp4_matmul",
 )
 
 
@@ -50,6 +52,10 @@ class moe_config(ctypes.Structure):
         ("alpha", ctypes.c_float), ("dtype", ctypes.c_int32), ("bias_mode", ctypes.c_int32),
         ("capacity_priority", ctypes.c_int32), ("overflow_mode", ctypes.c_int32),
     ]
+
+
+class moe_mxfp4_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n", "k", "n_mats", "n_seg", "activation", "out_dtype")]
 
 
 class moe_backward_io(ctypes.Structure):
@@ -88,7 +94,9 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P = ctypes.c_void_p
         cfgp = ctypes.POINTER(moe_config)
+        shp = ctypes.POINTER(moe_mxfp4_shape)
         I = ctypes.c_int
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
         sig = {
             "moe_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t)],
             "moe_buffer_rows": [cfgp] + [ctypes.POINTER(ctypes.c_int32)] * 4,
@@ -108,6 +116,12 @@ def lib() -> ctypes.CDLL:
             "moe_backward_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t)],
             "moe_layer_backward": [cfgp, ctypes.c_float, ctypes.POINTER(moe_backward_io), P, P],
             "moe_expert_ffn_segments": [cfgp, P, P, P, P, ctypes.c_int32] + [P] * 9,
+            "moe_mxfp4_quantize": [P, i32, i64, i32, P, P, P],
+            "moe_mxfp4_dequantize": [P, P, i64, i32, P, i32, P],
+            "moe_mxfp4_workspace_size": [shp, ctypes.POINTER(ctypes.c_size_t)],
+            "moe_mxfp4_workspace_init": [shp, P, P],
+            "moe_mxfp4_get_device_status": [shp, P, P, ctypes.POINTER(i32), i32],
+            "moe_mxfp4_matmul": [shp] + [P] * 11,
         }
         restype = {"moe_status_string": ctypes.c_char_p, "moe_kernel_launches": ctypes.c_uint64}
         for name, args in sig.items():
@@ -276,6 +290,67 @@ def moe_dispatch_noalloc(cfg, x, topk_idx, counts, kept, offsets, slot_row, row_
     _check(lib().moe_dispatch_noalloc(ctypes.byref(cfg), _p(x), _p(topk_idx), _p(counts), _p(kept),
                                       _p(offsets), _p(slot_row), _p(row_slot), _p(x_disp),
                                       _p(x_disp_scales), _stream(stream)), "moe_dispatch_noalloc")
+
+
+def _mxfp4_args(dense, codes, scales, what: str):
+    """(dtype, rows, cols) of a dense matrix and its MXFP4 form, checked against each other."""
+    import torch
+    dtypes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    if dense.dtype not in dtypes:
+        raise ValueError(f"{what}: the dense matrix must be float32 or bfloat16")
+    if dense.dim() < 1 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{what}: codes and scales are uint8 matrices")
+    cols = dense.shape[-1]
+    if cols < 1 or cols % 32:
+        raise ValueError(f"{what}: the last dimension ({cols}) must be a multiple of 32")
+    if codes.numel() * 2 != dense.numel() or scales.numel() * 32 != dense.numel():
+        raise ValueError(f"{what}: codes need (..., cols / 2) and scales (..., cols / 32) elements")
+    if not dense.device == codes.device == scales.device:
+        raise ValueError(f"{what}: all tensors must be on one device")
+    return dtypes[dense.dtype], dense.numel() // cols, cols
+
+
+def moe_mxfp4_quantize(x, codes, scales, stream=None):
+    """x (..., cols) float32 / bfloat16 into MXFP4: codes uint8 (..., cols / 2), scales uint8 (..., cols / 32)."""
+    dtype, rows, cols = _mxfp4_args(x, codes, scales, "moe_mxfp4_quantize")
+    _check(lib().moe_mxfp4_quantize(_p(x), dtype, rows, cols, _p(codes), _p(scales), _stream(stream)),
+           "moe_mxfp4_quantize")
+
+
+def moe_mxfp4_dequantize(codes, scales, out, stream=None):
+    """The values of an MXFP4 matrix into out (..., cols) float32 / bfloat16."""
+    dtype, rows, cols = _mxfp4_args(out, codes, scales, "moe_mxfp4_dequantize")
+    _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _p(out), dtype, _stream(stream)),
+           "moe_mxfp4_dequantize")
+
+
+def make_mxfp4_shape(rows: int, n: int, k: int, n_mats: int = 1, n_seg: int = 1, activation: int = MOE_ACT_NONE,
+                     out_dtype: int = MOE_BF16) -> moe_mxfp4_shape:
+    return moe_mxfp4_shape(rows, n, k, n_mats, n_seg, activation, out_dtype)
+
+
+def moe_mxfp4_workspace_size(shape: moe_mxfp4_shape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_mxfp4_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "moe_mxfp4_workspace_size")
+    return n.value
+
+
+def moe_mxfp4_workspace_init(shape, ws, stream=None):
+    _check(lib().moe_mxfp4_workspace_init(ctypes.byref(shape), _p(ws), _stream(stream)), "moe_mxfp4_workspace_init")
+
+
+def moe_mxfp4_get_device_status(shape, ws, stream=None, clear: bool = False) -> int:
+    st = ctypes.c_int32(0)
+    _check(lib().moe_mxfp4_get_device_status(ctypes.byref(shape), _p(ws), _stream(stream), ctypes.byref(st),
+                                             1 if clear else 0), "moe_mxfp4_get_device_status")
+    return st.value
+
+
+def moe_mxfp4_matmul(shape, a, a_scales, seg_offsets, seg_mat, w, w_scales, bias, y, y_scales, ws, stream=None):
+    """y[r] = act(W_e a[r] + bias_e) over segments of rows, both operands in MXFP4 (shape: make_mxfp4_shape)."""
+    _check(lib().moe_mxfp4_matmul(ctypes.byref(shape), _p(a), _p(a_scales), _p(seg_offsets), _p(seg_mat), _p(w),
+                                  _p(w_scales), _p(bias), _p(y), _p(y_scales), _p(ws), _stream(stream)),
+           "moe_mxfp4_matmul")
 
 
 class MoELayer:

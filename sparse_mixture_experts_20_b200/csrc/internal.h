@@ -160,6 +160,16 @@ cudaError_t launch_grouped_ffn_bf16_pair(const Dims& dm, const GemmArgs& a, cuda
 bool gemm_pairs_enabled();
 cudaError_t launch_grouped_ffn_fp8(const Dims& dm, const GemmArgs& a, cudaStream_t st);
 
+// MXFP4 (mxfp4.cu, mxfp4_matmul.cu); elems: a positive multiple of 32.
+cudaError_t launch_mxfp4_quantize(const void* x, int dtype, long long elems, uint8_t* codes, uint8_t* scales,
+                                  cudaStream_t st);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, long long elems, void* out,
+                                    int dtype, cudaStream_t st);
+cudaError_t launch_mxfp4_matmul(const moe_mxfp4_shape& s, const uint8_t* a, const uint8_t* a_scales,
+                                const int32_t* seg_offsets, const int32_t* seg_mat, const uint8_t* w,
+                                const uint8_t* w_scales, const float* bias, void* y, uint8_t* y_scales,
+                                int32_t* status, cudaStream_t st);
+
 cudaError_t launch_wait_selftest(int64_t timeout_ns, int32_t* status, cudaStream_t st);
 
 // TMA tensor maps (tma_host.cu).  `map` points at a CUtensorMap.

@@ -146,6 +146,17 @@ RouterScratch router_scratch(void* ws, const WsLayout& L) {
     return rs;
 }
 
+// Synchronises st and reads (and with clear resets) a device status word.
+int read_status(int32_t* dev, cudaStream_t st, int32_t* status, int32_t clear) {
+    cudaError_t e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = cudaMemcpy(status, dev, sizeof(int32_t), cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && clear) {
+        e = cudaMemsetAsync(dev, 0, sizeof(int32_t), st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    }
+    return cuda_status(e);
+}
+
 // Builds the two grouped-GEMM launches of the expert FFN and runs them.
 // seg_mat (device, n_seg entries) or nullptr: the routed group is n_seg
 // caller-made segments over x_disp (offsets has n_seg + 1 entries), segment i
@@ -320,15 +331,7 @@ int moe_get_device_status(const moe_config* cfg, void* ws, void* stream, int32_t
     const int v = validate(cfg, &dm);
     if (v != MOE_OK) return v;
     if (!ws || !status) return MOE_ERR_INVALID_ARG;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int32_t* dev = at<int32_t>(ws, ws_layout(dm).status);
-    cudaError_t e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess) e = cudaMemcpy(status, dev, sizeof(int32_t), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess && clear) {
-        e = cudaMemsetAsync(dev, 0, sizeof(int32_t), st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    return cuda_status(e);
+    return read_status(at<int32_t>(ws, ws_layout(dm).status), static_cast<cudaStream_t>(stream), status, clear);
 }
 
 int moe_last_cuda_error(void) { return g_last_cuda_error; }
@@ -510,6 +513,86 @@ int moe_layer_backward(const moe_config* cfg, float lam, const moe_backward_io* 
         for (const void* p : sh) if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
     }
     return cuda_status(launch_backward(dm, lam, *io, bws, static_cast<cudaStream_t>(stream)));
+}
+
+// elements of a (rows, cols) matrix, or -1 where the quantiser's grid or a
+// 64-bit size would not hold them
+static int mxfp4_elems(int64_t rows, int32_t cols, int32_t dtype, long long* elems) {
+    if (rows < 0 || cols < 1 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+    if (cols % 32 || rows > (1ll << 42) / cols) return MOE_ERR_UNSUPPORTED;
+    *elems = static_cast<long long>(rows) * cols;
+    return MOE_OK;
+}
+
+int moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+    NvtxRange nvtx("moe_mxfp4_quantize");
+    long long elems = 0;
+    const int v = mxfp4_elems(rows, cols, dtype, &elems);
+    if (v != MOE_OK) return v;
+    if (elems == 0) return MOE_OK;
+    if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_mxfp4_quantize(x, dtype, elems, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* out,
+                         int32_t dtype, void* stream) {
+    NvtxRange nvtx("moe_mxfp4_dequantize");
+    long long elems = 0;
+    const int v = mxfp4_elems(rows, cols, dtype, &elems);
+    if (v != MOE_OK) return v;
+    if (elems == 0) return MOE_OK;
+    if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_mxfp4_dequantize(codes, scales, elems, out, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+static int mxfp4_validate(const moe_mxfp4_shape* s) {
+    if (!s || s->rows < 0 || s->n < 1 || s->k < 1 || s->n_mats < 1 || s->n_seg < 1) return MOE_ERR_INVALID_ARG;
+    if (s->activation != MOE_ACT_NONE && s->activation != MOE_ACT_SILU) return MOE_ERR_INVALID_ARG;
+    if (s->out_dtype != MOE_F32 && s->out_dtype != MOE_BF16 && s->out_dtype != MOE_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (s->n % 32 || s->k % 128 || s->n_mats > 65535 || s->n_seg > 256) return MOE_ERR_UNSUPPORTED;
+    // tiles are counted in 32 bits: at most rows / 128 + n_seg of them per 256 columns
+    const long long tiles = (static_cast<long long>(s->rows) / 128 + s->n_seg) * ((s->n + 255) / 256);
+    return tiles > (1ll << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int moe_mxfp4_workspace_size(const moe_mxfp4_shape* shape, size_t* bytes) {
+    const int v = mxfp4_validate(shape);
+    if (v != MOE_OK) return v;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = 256;
+    return MOE_OK;
+}
+
+int moe_mxfp4_workspace_init(const moe_mxfp4_shape* shape, void* ws, void* stream) {
+    const int v = mxfp4_validate(shape);
+    if (v != MOE_OK) return v;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(cudaMemsetAsync(ws, 0, 256, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_mxfp4_get_device_status(const moe_mxfp4_shape* shape, void* ws, void* stream, int32_t* status,
+                                int32_t clear) {
+    const int v = mxfp4_validate(shape);
+    if (v != MOE_OK) return v;
+    if (!ws || !status) return MOE_ERR_INVALID_ARG;
+    return read_status(static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream), status, clear);
+}
+
+int moe_mxfp4_matmul(const moe_mxfp4_shape* shape, const uint8_t* a, const uint8_t* a_scales,
+                     const int32_t* seg_offsets, const int32_t* seg_mat, const uint8_t* w, const uint8_t* w_scales,
+                     const float* bias, void* y, uint8_t* y_scales, void* ws, void* stream) {
+    NvtxRange nvtx("moe_mxfp4_matmul");
+    const int v = mxfp4_validate(shape);
+    if (v != MOE_OK) return v;
+    if (shape->rows == 0) return MOE_OK;
+    const void* need[] = {a, a_scales, seg_offsets, seg_mat, w, w_scales, y};
+    for (const void* p : need) if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (bias && !aligned16(bias)) return MOE_ERR_INVALID_ARG;
+    if ((shape->out_dtype == MOE_MXFP4) != (y_scales != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_mxfp4_matmul(*shape, a, a_scales, seg_offsets, seg_mat, w, w_scales, bias, y, y_scales,
+                                           static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 int moe_selftest_wait_timeout(const moe_config* cfg, int64_t timeout_ns, void* ws, void* stream) {

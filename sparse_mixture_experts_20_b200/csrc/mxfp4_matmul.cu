@@ -1,0 +1,451 @@
+// Grouped product of MXFP4 operands on tcgen05: y[r] = act(W_e a[r] + b_e)
+// for the rows r of each segment and the segment's matrix e.
+//
+// tcgen05.mma kind::mxf4.block_scale.scale_vec::2X multiplies packed E2M1
+// operands, 64 elements of K per instruction, and applies one E8M0 scale per
+// row (of A) and column (of B) per 32 elements from tensor memory; the
+// accumulator sums sa * sb * (a . b) over the whole K loop in fp32.
+//
+// Tiles are 128 rows x 256 weight rows, one persistent CTA per SM, the
+// segment table and tile order of ffn_common.cuh.  The two accumulators
+// overlap in tensor memory (columns 0..255 and 192..447) and the scales take
+// columns 448..495: two slots of 24, used in turn by the K stages.  The
+// epilogue drains the 64 overlapping columns first.
+//
+// Per CTA (320 threads):
+//   warp 0      TMA producer: 128 bytes of K (256 elements) per stage, A 16 KB
+//               and B 32 KB;
+//   warp 1      MMA issuer: per stage copies the scales from shared to tensor
+//               memory (tcgen05.cp 32x128b.warpx4, in order with the MMAs),
+//               then 4 MMAs of K = 64;
+//   warps 2..5  epilogue: bias, SiLU, and bf16, fp32 or MXFP4 rows (a chunk
+//               of 32 columns per tcgen05.ld is one block of the output);
+//   warps 6..9  scale loaders: a thread reads the 8 scale bytes of its A row
+//               and of two weight rows for a stage and lays them out in shared
+//               memory as tcgen05.cp reads them: 512 bytes per 128 rows and
+//               128 elements of K, row r's four bytes at
+//               16 (r mod 32) + 4 (r div 32).
+// Every wait is bounded (common.cuh).
+#include "ffn_common.cuh"
+#include "mxfp4.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ffn;
+
+constexpr int NUM_THREADS = 320;
+constexpr int BN = 256, BKB = 128;                   // weight rows per tile; bytes of K per stage (256 elements)
+constexpr int STAGES = 4;
+constexpr uint32_t TMEM_COLS = 512, ACC1_COL = 192, SF_COL0 = 448, SF_STRIDE = 24;
+constexpr uint32_t FULL_ARRIVALS = 1 + 4;            // TMA expect_tx + one lane per loader warp
+constexpr int LOOKAHEAD = 2;                         // stages of scales a loader has in flight in registers
+constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
+constexpr uint64_t kDrainTimeoutNs = 200000000ull;
+
+constexpr int A_BYTES = BM * BKB, B_BYTES = BN * BKB;
+constexpr int SF_BYTES = 2 * 3 * 512;                // per half stage: A, B rows 0..127, B rows 128..255
+constexpr int OFF_A = 0;
+constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
+constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
+constexpr int OFF_BAR = OFF_SF + STAGES * SF_BYTES;
+constexpr int N_BARS = 2 * STAGES + 4 + 2;           // full, empty [STAGES]; accf, acce [2]; ovl; drain
+constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
+constexpr int OFF_SEG = OFF_MISC + 16;
+constexpr int OFF_BIAS = (OFF_SEG + SegTable::SEG_INTS * 4 + 15) & ~15;   // per epilogue warp, 2 x BN fp32
+constexpr int TOTAL = OFF_BIAS + 4 * 2 * BN * 4;
+constexpr int ALLOC = TOTAL + 1024;
+static_assert(ALLOC <= 227 * 1024, "shared memory budget");
+static_assert(OFF_SF % 128 == 0 && OFF_BAR % 8 == 0, "alignment");
+static_assert(SF_COL0 + 2 * SF_STRIDE <= TMEM_COLS, "tensor memory budget");
+
+struct __align__(64) Mx4Params {
+    TcParams tc;              // a_map[0], b_map[0] over bytes; g[0].K, N in elements
+    const uint8_t* a_scales;  // (rows, K/32)
+    const uint8_t* w_scales;  // (n_mats, N, K/32)
+    uint8_t* y_scales;        // (rows, N/32), MXFP4 output
+};
+
+// Instruction descriptor of kind::mxf4.block_scale: E2M1 A and B (format 1,
+// bits 7-9 and 10-11), N >> 3 (17-22), UE8M0 scales (bit 23), M >> 7 (27-28),
+// and the byte offset (0 or 2) of the two scales of an MMA in its columns'
+// words (bits 4-5 for B, 29-30 for A).
+__host__ __device__ constexpr uint32_t make_idesc_mxf4(uint32_t sf_byte) {
+    return (sf_byte << 4) | (1u << 7) | (1u << 10) | ((BN >> 3) << 17) | (1u << 23) | ((BM >> 7) << 27) |
+           (sf_byte << 29);
+}
+
+__device__ __forceinline__ void umma_mxf4_bs(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+        : "memory");
+}
+
+// 32 rows x 16 bytes (512 contiguous bytes of shared memory, groups of 8 rows
+// 128 bytes apart) to 4 columns of tensor memory, the same in every lane
+// quadrant.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, const void* src) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_u32(src) & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(128u >> 4) << 16;
+    d |= static_cast<uint64_t>(128u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(d) : "memory");
+}
+
+// The MMA thread's wait for a full stage: bounded, polling without the
+// suspend hint (this thread is on the critical path).
+static __device__ __noinline__ bool mma_wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                  int32_t* status, uint64_t timeout_ns) {
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (global_timer_ns() - t0 > timeout_ns) {
+                *abort_flag = 1;
+                set_device_status(status, MOE_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+struct Item {
+    int tile, kb;
+    TileInfo ti;
+};
+
+// OUT: MOE_F32, MOE_BF16 or MOE_MXFP4 rows.
+template <int OUT>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
+    const TcParams& p = mp.tc;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t* empty = full + STAGES;
+    uint64_t* accf = empty + STAGES;
+    uint64_t* acce = accf + 2;
+    uint64_t* ovl = acce + 2;
+    uint64_t* drain = ovl + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+    SegTable seg(reinterpret_cast<int*>(smem + OFF_SEG));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 0) tmem_alloc<TMEM_COLS>(tmem_slot);
+    if (warp == 1 && lane == 0) {
+        for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], FULL_ARRIVALS); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], 128); }
+        mbar_init(ovl, 128);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) { tma_prefetch_desc(&p.a_map[0]); tma_prefetch_desc(&p.b_map[0]); }
+    pdl_wait();
+    pdl_allow_next();
+    const int nseg = build_seg_table<BN>(p, seg, NUM_THREADS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total_tiles = seg.start[nseg];
+    const int K = p.g[0].K, N = p.g[0].N;
+    const int kblocks = ceil_div(K, 2 * BKB);
+
+    if (warp == 0) {
+        // ================= TMA producer
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
+                const TileInfo ti = decode_tile<BN, 2 * BKB>(tile, p, seg, nseg);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&full[stage], A_BYTES + B_BYTES);
+                    tma_load_2d(smem + OFF_A + stage * A_BYTES, &p.a_map[0], &full[stage], kb * BKB, ti.a_row);
+                    tma_load_3d(smem + OFF_B + stage * B_BYTES, &p.b_map[0], &full[stage], kb * BKB, ti.n0, ti.mat);
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (!ok) {
+                // copies in flight land before the CTA gives its memory back
+                int s = stage;
+                uint32_t ph = phase;
+                const int pending = issued < STAGES ? issued : STAGES;
+                for (int i = 0; i < pending; ++i) {
+                    if (--s < 0) { s = STAGES - 1; ph ^= 1u; }
+                    volatile int no_abort = 0;
+                    mbar_wait_bounded(&full[s], ph, &no_abort, nullptr, kDrainTimeoutNs);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer
+        if (lane == 0) {
+            int stage = 0, abuf = 0;
+            uint32_t phase = 0, aph0 = 0, aph1 = 0, ovl_ph = 0;
+            long long item = 0;
+            bool ok = true, issued_any = false, first = true;
+            for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
+                // the previous tile's overlapping columns drained, and this
+                // buffer's tile from two tiles back fully drained
+                if (!first) {
+                    if (!mbar_wait_bounded(ovl, ovl_ph, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                    ovl_ph ^= 1u;
+                }
+                first = false;
+                uint32_t& aph = abuf ? aph1 : aph0;
+                if (!mbar_wait_bounded(&acce[abuf], aph ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (abuf ? ACC1_COL : 0u);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_try_wait(&full[stage], phase) &&
+                        !mma_wait_spin(&full[stage], phase, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                    // the MMAs that read this scale slot two stages ago are done
+                    if (item >= 2) {
+                        const int s2 = (stage + STAGES - 2) % STAGES;
+                        const uint32_t ph2 = stage >= 2 ? phase : phase ^ 1u;
+                        if (!mbar_try_wait(&empty[s2], ph2) &&
+                            !mma_wait_spin(&empty[s2], ph2, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                    }
+                    ++item;
+                    tc_fence_after();
+                    const uint64_t adesc = smem_desc_k_sw128(smem + OFF_A + stage * A_BYTES);
+                    const uint64_t bdesc = smem_desc_k_sw128(smem + OFF_B + stage * B_BYTES);
+                    const uint8_t* sf = smem + OFF_SF + stage * SF_BYTES;
+                    const uint32_t slot = tmem_base + SF_COL0 + static_cast<uint32_t>(stage & 1) * SF_STRIDE;
+#pragma unroll
+                    for (int j = 0; j < 6; ++j) tmem_cp_scales(slot + 4 * j, sf + 512 * j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {          // 4 x 64 elements of K per stage
+                        const uint32_t s = slot + 12 * (k >> 1);
+                        umma_mxf4_bs(d_tmem, adesc + 2 * k, bdesc + 2 * k, make_idesc_mxf4(2 * (k & 1)), s, s + 4,
+                                     (kb > 0 || k > 0) ? 1u : 0u);
+                    }
+                    issued_any = true;
+                    umma_commit(&empty[stage]);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit(&accf[abuf]);
+                aph ^= 1u;
+                abuf ^= 1;
+            }
+            if (!ok && issued_any) {
+                umma_commit(drain);
+                volatile int no_abort = 0;
+                mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainTimeoutNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        // ================= epilogue (warps 2..5)
+        const int quad = warp & 3;
+        const int r_local = quad * 32 + lane;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        int abuf = 0;
+        uint32_t fph0 = 0, fph1 = 0;
+        for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x) {
+            const TileInfo ti = decode_tile<BN, 2 * BKB>(tile, p, seg, nseg);
+            const GroupDev& g = p.g[0];
+            const bool row_ok = r_local < ti.rows_left;
+            float* bias_s = reinterpret_cast<float*>(smem + OFF_BIAS) + (quad * 2 + abuf) * BN;
+#pragma unroll
+            for (int i = 4 * lane; i < BN; i += 128) {
+                const float4 v = (g.bias && ti.n0 + i < N)
+                    ? __ldg(reinterpret_cast<const float4*>(g.bias + static_cast<size_t>(ti.mat) * N + ti.n0 + i))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4*>(bias_s + i) = v;
+            }
+            __syncwarp();
+            uint32_t& fph = abuf ? fph1 : fph0;
+            if (!warp_wait(&accf[abuf], fph, abort_flag, p.status, p.timeout_ns, lane)) break;
+            fph ^= 1u;
+            tc_fence_after();
+            const uint32_t acc = lane_base + (abuf ? ACC1_COL : 0u);
+            const size_t row = static_cast<size_t>(ti.c_row + r_local);
+            // chunks of 32 columns, the overlapping ones (6, 7 of buffer 0;
+            // 0, 1 of buffer 1) first
+#pragma unroll 1
+            for (int ci = 0; ci < BN / 32; ++ci) {
+                const int c = abuf ? ci : (ci + 6) & 7;
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c * 32), r);
+                tmem_ld_wait_regs(r);
+                if (ci == 1) { tc_fence_before(); mbar_arrive(ovl); }
+                else if (ci == BN / 32 - 1) { tc_fence_before(); mbar_arrive(&acce[abuf]); }
+                const int n = ti.n0 + c * 32;
+                if (!row_ok || n >= N) continue;
+                float v[32];
+                const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 b = b4[j];
+                    v[4 * j + 0] = __uint_as_float(r[4 * j + 0]) + b.x;
+                    v[4 * j + 1] = __uint_as_float(r[4 * j + 1]) + b.y;
+                    v[4 * j + 2] = __uint_as_float(r[4 * j + 2]) + b.z;
+                    v[4 * j + 3] = __uint_as_float(r[4 * j + 3]) + b.w;
+                }
+                if (p.silu) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
+                }
+                if constexpr (OUT == MOE_F32) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.C) + row * N + n);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                } else if constexpr (OUT == MOE_BF16) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.C) + row * N + n);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * q + 2 * h], v[8 * q + 2 * h + 1]);
+                            w[h] = *reinterpret_cast<uint32_t*>(&t);
+                        }
+                        dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+                    const uint32_t sb = mxfp4_scale_byte(m);
+                    const float inv = mxfp4_inv_scale(sb == 255u ? 127u : sb);
+                    uint32_t w[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float t[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) t[j] = v[8 * q + j] * inv;
+                        w[q] = sb == 255u ? 0u : f32x8_to_e2m1x8(t);
+                    }
+                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + (row * N + n) / 2) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                    mp.y_scales[(row * N + n) / 32] = static_cast<uint8_t>(sb);
+                }
+            }
+            abuf ^= 1;
+        }
+    } else {
+        // ================= scale loaders (warps 6..9): thread i has A row i and weight rows i, 128 + i
+        const int i = tid - 6 * 32;
+        const int kq = K / 32;                           // scale bytes per row, a multiple of 4
+        uint32_t* dst0 = reinterpret_cast<uint32_t*>(smem + OFF_SF + 16 * (i & 31) + 4 * (i >> 5));
+        auto start = [&](Item& it) {
+            it.tile = blockIdx.x;
+            it.kb = 0;
+            if (it.tile < total_tiles) it.ti = decode_tile<BN, 2 * BKB>(it.tile, p, seg, nseg);
+        };
+        auto advance = [&](Item& it) {
+            if (++it.kb >= kblocks) {
+                it.kb = 0;
+                it.tile += gridDim.x;
+                if (it.tile < total_tiles) it.ti = decode_tile<BN, 2 * BKB>(it.tile, p, seg, nseg);
+            }
+        };
+        // rows and columns past the end read as 2^0 (their codes read as zero)
+        auto load = [&](const Item& it, uint32_t (&s)[6]) {
+            const int k0 = it.kb * 8;
+            const bool two = k0 + 4 < kq;
+            auto row = [&](const uint8_t* base, bool ok, uint32_t& lo, uint32_t& hi) {
+                lo = ok ? __ldg(reinterpret_cast<const uint32_t*>(base + k0)) : 0x7F7F7F7Fu;
+                hi = ok && two ? __ldg(reinterpret_cast<const uint32_t*>(base + k0 + 4)) : 0x7F7F7F7Fu;
+            };
+            row(mp.a_scales + static_cast<size_t>(it.ti.a_row + i) * kq, i < it.ti.rows_left, s[0], s[3]);
+            const uint8_t* w = mp.w_scales + (static_cast<size_t>(it.ti.mat) * N + it.ti.n0 + i) * kq;
+            row(w, it.ti.n0 + i < N, s[1], s[4]);
+            row(w + static_cast<size_t>(128) * kq, it.ti.n0 + 128 + i < N, s[2], s[5]);
+        };
+        Item cur, ahead;
+        start(cur);
+        start(ahead);
+        uint32_t ring[LOOKAHEAD][6];
+#pragma unroll
+        for (int j = 0; j < LOOKAHEAD; ++j)
+            if (ahead.tile < total_tiles) { load(ahead, ring[j]); advance(ahead); }
+        int stage = 0;
+        uint32_t phase = 0;
+        bool aborted = false;
+#pragma unroll 1
+        while (cur.tile < total_tiles && !aborted) {
+#pragma unroll
+            for (int j = 0; j < LOOKAHEAD; ++j) {
+                if (cur.tile >= total_tiles) break;
+                if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.timeout_ns, lane)) {
+                    aborted = true;
+                    break;
+                }
+                uint32_t* dst = dst0 + stage * (SF_BYTES / 4);
+#pragma unroll
+                for (int q = 0; q < 6; ++q) dst[q * 128] = ring[j][q];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[stage]);
+                if (ahead.tile < total_tiles) { load(ahead, ring[j]); advance(ahead); }
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                advance(cur);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc<TMEM_COLS>(tmem_base);
+    }
+}
+
+template <int OUT>
+cudaError_t launch_out(const Mx4Params& p, cudaStream_t st) {
+    auto kernel = mxfp4_matmul_kernel<OUT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ALLOC);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(device_sm_count()), dim3(NUM_THREADS), ALLOC, st, 1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_matmul(const moe_mxfp4_shape& s, const uint8_t* a, const uint8_t* a_scales,
+                                const int32_t* seg_offsets, const int32_t* seg_mat, const uint8_t* w,
+                                const uint8_t* w_scales, const float* bias, void* y, uint8_t* y_scales,
+                                int32_t* status, cudaStream_t st) {
+    Mx4Params p;
+    std::memset(&p, 0, sizeof(p));
+    GroupDev& g = p.tc.g[0];
+    g.n_mats = s.n_seg;
+    g.offsets = seg_offsets;
+    g.bias = bias;
+    g.C = y;
+    g.N = s.n;
+    g.K = s.k;
+    g.a_rows = s.rows;
+    g.seg_mat = seg_mat;
+    g.n_weights = s.n_mats;
+    p.tc.silu = s.activation == MOE_ACT_SILU;
+    p.tc.status = status;
+    p.tc.timeout_ns = kWaitTimeoutNs;
+    p.a_scales = a_scales;
+    p.w_scales = w_scales;
+    p.y_scales = y_scales;
+    if (!encode_tma_2d(&p.tc.a_map[0], a, s.rows, s.k / 2, 1, BM) ||
+        !encode_tma_3d(&p.tc.b_map[0], w, s.n_mats, s.n, s.k / 2, 1, BN))
+        return cudaErrorInvalidValue;
+    if (s.out_dtype == MOE_F32) return launch_out<MOE_F32>(p, st);
+    if (s.out_dtype == MOE_BF16) return launch_out<MOE_BF16>(p, st);
+    return launch_out<MOE_MXFP4>(p, st);
+}
+
+}  // namespace moe
