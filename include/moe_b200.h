@@ -92,8 +92,9 @@ extern "C" {
 #define MOE_BF16            1   /* bf16 activations and weights, fp32 accumulate */
 #define MOE_FP8_E4M3_BLOCK  2   /* e4m3 dispatch + weights with block scales,
                                    bf16 expert outputs and layer output          */
-#define MOE_MXFP4           3   /* MXFP4 operands (moe_mxfp4_*); the layer's entry
-                                   points reject it                              */
+#define MOE_MXFP4           3   /* MXFP4 expert weights (moe_layer_forward_few) or
+                                   operands (moe_mxfp4_*); the other entry points
+                                   reject it                                     */
 
 /* Layer shape.  Mirrors the reference module's constructor
  * (d_model, n_routed, n_shared, top_k, d_ff) plus the batch size, the shared
@@ -293,6 +294,47 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
                       const void* W2, const float* W2_scales, const float* b2,
                       const void* Ws1, const float* Ws1_scales, const float* bs1,
                       const void* Ws2, const float* Ws2_scales, const float* bs2,
+                      void* out, float* f, float* P, float* loss,
+                      int32_t* topk_idx, float* gates, int32_t* counts,
+                      void* ws, void* stream);
+
+/* ---- the layer for a few tokens ---------------------------------------------
+ * moe_layer_forward for 1 <= T <= MOE_FEW_MAX_TOKENS in ONE kernel: the
+ * decoding step, whose time is the bytes of the experts the tokens reach.
+ * Same arguments, same formulas and same outputs as moe_layer_forward
+ * (routing, capacity, overflow, balance statistics included), except that a
+ * slot's output is not rounded to bf16 before the gate-weighted sum.
+ *   dtype MOE_BF16            weights bf16; the hidden activation is rounded
+ *                             to bf16 between the layers
+ *   dtype MOE_FP8_E4M3_BLOCK  e4m3 weights, W*_scales fp32 (E, rows/128,
+ *                             cols/128); x and the hidden activation are
+ *                             quantised to e4m3 per 128 columns
+ *   dtype MOE_MXFP4           weights as moe_mxfp4_quantize writes them:
+ *                             W1 (N_r, d_ff, d_model/2) bytes with W1_scales
+ *                             (N_r, d_ff, d_model/32) bytes, W2 (N_r, d_model,
+ *                             d_ff/2) with W2_scales (N_r, d_model, d_ff/32),
+ *                             the shared experts likewise; x (bf16) and the
+ *                             hidden activation are not quantised (held in
+ *                             fp16 with a power-of-two scale per 128 columns)
+ * In every mode x and out are bf16, biases and W_r fp32.
+ * Errors: MOE_ERR_UNSUPPORTED for MOE_F32, for T > MOE_FEW_MAX_TOKENS, and for
+ * d_model or a d_ff that is not a multiple of 64 (bf16) or 128.
+ * ws: moe_few_workspace_size() bytes, 256-byte aligned, zero-filled once by
+ * moe_few_workspace_init before first use and left consistent by every call;
+ * calls that overlap on the GPU need one each.  moe_get_device_status reads
+ * its status word (MOE_DEV_TIMEOUT: a bounded wait gave up and the outputs are
+ * incomplete).  The kernel is launched cooperatively, one block per SM: it
+ * starts once every block fits on the device.  Launches can be captured into
+ * a graph. */
+#define MOE_FEW_MAX_TOKENS 16
+MOE_EXPORT int moe_few_workspace_size(const moe_config* cfg, size_t* bytes);
+MOE_EXPORT int moe_few_workspace_init(const moe_config* cfg, void* ws, void* stream);
+MOE_EXPORT int moe_layer_forward_few(const moe_config* cfg, const void* x, const float* W_r,
+                      const float* logit_bias,
+                      const void* W1, const void* W1_scales, const float* b1,
+                      const void* W2, const void* W2_scales, const float* b2,
+                      const void* Ws1, const void* Ws1_scales, const float* bs1,
+                      const void* Ws2, const void* Ws2_scales, const float* bs2,
                       void* out, float* f, float* P, float* loss,
                       int32_t* topk_idx, float* gates, int32_t* counts,
                       void* ws, void* stream);

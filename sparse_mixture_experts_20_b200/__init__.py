@@ -30,6 +30,7 @@ MOE_DEV_BAD_ROUTING = 0x1
 MOE_DEV_TIMEOUT = 0x2
 MOE_F32, MOE_BF16, MOE_FP8_E4M3_BLOCK, MOE_MXFP4 = 0, 1, 2, 3
 MOE_ACT_NONE, MOE_ACT_SILU = 0, 1
+MOE_FEW_MAX_TOKENS = 16
 MOE_BIAS_LOGITS, MOE_BIAS_SELECTION = 0, 1
 MOE_PRIORITY_TOKEN, MOE_PRIORITY_SLOT = 0, 1
 MOE_OVERFLOW_DROP, MOE_OVERFLOW_PASS = 0, 1
@@ -39,7 +40,8 @@ EXPORTED = (
     "moe_last_cuda_error", "moe_status_string", "moe_route", "moe_dispatch", "moe_expert_ffn",
     "moe_combine", "moe_balance_stats", "moe_layer_forward", "moe_selftest_wait_timeout",
     "moe_dispatch_noalloc", "moe_kernel_launches", "moe_backward_workspace_size", "moe_layer_backward",
-    "moe_expert_ffn_segments", "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_workspace_size",
+    "moe_expert_ffn_segments", "moe_few_workspace_size", "moe_few_workspace_init", "moe_layer_forward_few",
+    "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_workspace_size",
     "moe_mxfp4_workspace_init", "moe_mxfp4_get_device_status", "moe_mxfp4_matmul",
 )
 
@@ -116,6 +118,9 @@ def lib() -> ctypes.CDLL:
             "moe_backward_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t)],
             "moe_layer_backward": [cfgp, ctypes.c_float, ctypes.POINTER(moe_backward_io), P, P],
             "moe_expert_ffn_segments": [cfgp, P, P, P, P, ctypes.c_int32] + [P] * 9,
+            "moe_few_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t)],
+            "moe_few_workspace_init": [cfgp, P, P],
+            "moe_layer_forward_few": [cfgp] + [P] * 24,
             "moe_mxfp4_quantize": [P, i32, i64, i32, P, P, P],
             "moe_mxfp4_dequantize": [P, P, i64, i32, P, i32, P],
             "moe_mxfp4_workspace_size": [shp, ctypes.POINTER(ctypes.c_size_t)],
@@ -292,6 +297,28 @@ def moe_dispatch_noalloc(cfg, x, topk_idx, counts, kept, offsets, slot_row, row_
                                       _p(x_disp_scales), _stream(stream)), "moe_dispatch_noalloc")
 
 
+def moe_few_workspace_size(cfg: moe_config) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_few_workspace_size(ctypes.byref(cfg), ctypes.byref(n)), "moe_few_workspace_size")
+    return n.value
+
+
+def moe_few_workspace_init(cfg, ws, stream=None):
+    _check(lib().moe_few_workspace_init(ctypes.byref(cfg), _p(ws), _stream(stream)), "moe_few_workspace_init")
+
+
+def moe_layer_forward_few(cfg, x, W_r, logit_bias, W1, W1_scales, b1, W2, W2_scales, b2,
+                          Ws1, Ws1_scales, bs1, Ws2, Ws2_scales, bs2, out, f, P, loss,
+                          topk_idx, gates, counts, ws, stream=None):
+    """moe_layer_forward for at most MOE_FEW_MAX_TOKENS tokens, in one kernel (bf16, FP8 or MXFP4 experts);
+    ws: moe_few_workspace_size() bytes after moe_few_workspace_init."""
+    _check(lib().moe_layer_forward_few(ctypes.byref(cfg), _p(x), _p(W_r), _p(logit_bias), _p(W1), _p(W1_scales),
+                                       _p(b1), _p(W2), _p(W2_scales), _p(b2), _p(Ws1), _p(Ws1_scales), _p(bs1),
+                                       _p(Ws2), _p(Ws2_scales), _p(bs2), _p(out), _p(f), _p(P), _p(loss),
+                                       _p(topk_idx), _p(gates), _p(counts), _p(ws), _stream(stream)),
+           "moe_layer_forward_few")
+
+
 def _mxfp4_args(dense, codes, scales, what: str):
     """(dtype, rows, cols) of a dense matrix and its MXFP4 form, checked against each other."""
     import torch
@@ -359,7 +386,9 @@ class MoELayer:
     weights: dict with W_r, logit_bias (or None), W1, W1_scales, b1, W2,
     W2_scales, b2, Ws1, Ws1_scales, bs1, Ws2, Ws2_scales, bs2 (CUDA tensors or
     None where not used).  forward(x) runs moe_layer_forward on the current
-    stream and returns (out, f, P, loss).
+    stream and returns (out, f, P, loss); forward_few(x) is the same layer
+    through moe_layer_forward_few, for at most MOE_FEW_MAX_TOKENS tokens.  A
+    layer of MXFP4 experts has forward_few only.
     """
 
     def __init__(self, cfg: moe_config, weights: dict, device="cuda"):
@@ -367,8 +396,12 @@ class MoELayer:
         self.cfg = cfg
         self.w = weights
         self.device = torch.device(device)
-        self.ws = torch.empty(moe_workspace_size(cfg), dtype=torch.uint8, device=self.device)
-        moe_workspace_init(cfg, self.ws)
+        if cfg.dtype == MOE_MXFP4:
+            self.ws = self._few_workspace()
+        else:
+            self.ws = torch.empty(moe_workspace_size(cfg), dtype=torch.uint8, device=self.device)
+            moe_workspace_init(cfg, self.ws)
+        self._few_ws = self.ws if cfg.dtype == MOE_MXFP4 else None
         out_dt = torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16
         self.out = torch.empty((cfg.T, cfg.d_model), dtype=out_dt, device=self.device)
         self.f = torch.empty(cfg.n_routed, dtype=torch.float32, device=self.device)
@@ -385,6 +418,25 @@ class MoELayer:
                           g("W2"), g("W2_scales"), g("b2"), g("Ws1"), g("Ws1_scales"), g("bs1"),
                           g("Ws2"), g("Ws2_scales"), g("bs2"), self.out, self.f, self.P, self.loss,
                           self.topk_idx, self.gates, self.counts, self.ws, stream)
+        return self.out, self.f, self.P, self.loss
+
+    def _few_workspace(self):
+        import torch
+        ws = torch.empty(moe_few_workspace_size(self.cfg), dtype=torch.uint8, device=self.device)
+        moe_few_workspace_init(self.cfg, ws)
+        return ws
+
+    def forward_few(self, x, stream=None):
+        """forward(x) in one kernel, for T <= MOE_FEW_MAX_TOKENS.  The first call allocates and clears the
+        workspace (on the current stream): make it before capturing calls into a graph."""
+        if self._few_ws is None:
+            self._few_ws = self._few_workspace()
+        w = self.w
+        g = lambda k: w.get(k)  # noqa: E731
+        moe_layer_forward_few(self.cfg, x, g("W_r"), g("logit_bias"), g("W1"), g("W1_scales"), g("b1"),
+                              g("W2"), g("W2_scales"), g("b2"), g("Ws1"), g("Ws1_scales"), g("bs1"),
+                              g("Ws2"), g("Ws2_scales"), g("bs2"), self.out, self.f, self.P, self.loss,
+                              self.topk_idx, self.gates, self.counts, self._few_ws, stream)
         return self.out, self.f, self.P, self.loss
 
     def _forward_into(self, x, out, loss, stream=None):

@@ -160,6 +160,28 @@ cudaError_t launch_grouped_ffn_bf16_pair(const Dims& dm, const GemmArgs& a, cuda
 bool gemm_pairs_enabled();
 cudaError_t launch_grouped_ffn_fp8(const Dims& dm, const GemmArgs& a, cudaStream_t st);
 
+// The layer for a few tokens (few.cu): the arguments of moe_layer_forward_few.
+struct FewArgs {
+    const void* x;
+    const float* W_r;
+    const float* logit_bias;
+    const void *W1, *W1_scales;
+    const float* b1;
+    const void *W2, *W2_scales;
+    const float* b2;
+    const void *Ws1, *Ws1_scales;
+    const float* bs1;
+    const void *Ws2, *Ws2_scales;
+    const float* bs2;
+    void* out;
+    float *f, *P, *loss;
+    int32_t* topk_idx;
+    float* gates;
+    int32_t* counts;
+};
+size_t few_ws_bytes(const Dims& dm);
+cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t st);
+
 // MXFP4 (mxfp4.cu, mxfp4_matmul.cu); elems: a positive multiple of 32.
 cudaError_t launch_mxfp4_quantize(const void* x, int dtype, long long elems, uint8_t* codes, uint8_t* scales,
                                   cudaStream_t st);

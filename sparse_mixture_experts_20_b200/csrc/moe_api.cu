@@ -157,6 +157,22 @@ int read_status(int32_t* dev, cudaStream_t st, int32_t* status, int32_t clear) {
     return cuda_status(e);
 }
 
+// validate() for the few-token layer, which has no fp32 form and knows MXFP4
+// (block sizes as FP8: everything a multiple of 128).
+int validate_few(const moe_config* cfg, Dims* dm) {
+    if (!cfg) return MOE_ERR_INVALID_ARG;
+    moe_config c = *cfg;
+    if (c.dtype == MOE_MXFP4) c.dtype = MOE_FP8_E4M3_BLOCK;
+    const int v = validate(&c, dm);
+    if (v != MOE_OK) return v;
+    if (c.dtype == MOE_F32 || c.T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    // the rows of all experts are counted in 32 bits, 16 at a time
+    const long long rows = static_cast<long long>(dm->E) * dm->dff + static_cast<long long>(dm->S) * dm->dffs;
+    if (rows > (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+    dm->dtype = cfg->dtype;
+    return MOE_OK;
+}
+
 // Builds the two grouped-GEMM launches of the expert FFN and runs them.
 // seg_mat (device, n_seg entries) or nullptr: the routed group is n_seg
 // caller-made segments over x_disp (offsets has n_seg + 1 entries), segment i
@@ -328,10 +344,11 @@ int moe_workspace_init(const moe_config* cfg, void* ws, void* stream) {
 
 int moe_get_device_status(const moe_config* cfg, void* ws, void* stream, int32_t* status, int32_t clear) {
     Dims dm;
-    const int v = validate(cfg, &dm);
+    const int v = cfg && cfg->dtype == MOE_MXFP4 ? validate_few(cfg, &dm) : validate(cfg, &dm);
     if (v != MOE_OK) return v;
     if (!ws || !status) return MOE_ERR_INVALID_ARG;
-    return read_status(at<int32_t>(ws, ws_layout(dm).status), static_cast<cudaStream_t>(stream), status, clear);
+    // every workspace starts with its status word
+    return read_status(static_cast<int32_t*>(ws), static_cast<cudaStream_t>(stream), status, clear);
 }
 
 int moe_last_cuda_error(void) { return g_last_cuda_error; }
@@ -513,6 +530,51 @@ int moe_layer_backward(const moe_config* cfg, float lam, const moe_backward_io* 
         for (const void* p : sh) if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
     }
     return cuda_status(launch_backward(dm, lam, *io, bws, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_few_workspace_size(const moe_config* cfg, size_t* bytes) {
+    Dims dm;
+    const int v = validate_few(cfg, &dm);
+    if (v != MOE_OK) return v;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = few_ws_bytes(dm);
+    return MOE_OK;
+}
+
+int moe_few_workspace_init(const moe_config* cfg, void* ws, void* stream) {
+    Dims dm;
+    const int v = validate_few(cfg, &dm);
+    if (v != MOE_OK) return v;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(cudaMemsetAsync(ws, 0, few_ws_bytes(dm), static_cast<cudaStream_t>(stream)));
+}
+
+int moe_layer_forward_few(const moe_config* cfg, const void* x, const float* W_r, const float* logit_bias,
+                          const void* W1, const void* W1_scales, const float* b1,
+                          const void* W2, const void* W2_scales, const float* b2,
+                          const void* Ws1, const void* Ws1_scales, const float* bs1,
+                          const void* Ws2, const void* Ws2_scales, const float* bs2,
+                          void* out, float* f, float* P, float* loss,
+                          int32_t* topk_idx, float* gates, int32_t* counts, void* ws, void* stream) {
+    NvtxRange nvtx("moe_layer_forward_few");
+    Dims dm;
+    const int v = validate_few(cfg, &dm);
+    if (v != MOE_OK) return v;
+    const void* need[] = {x, W_r, W1, b1, W2, b2, out};
+    for (const void* p : need) if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (!f || !P || !loss || !ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
+    const bool scaled = dm.dtype != MOE_BF16;
+    if (scaled && (!W1_scales || !W2_scales || !aligned16(W1_scales) || !aligned16(W2_scales)))
+        return MOE_ERR_INVALID_ARG;
+    if (dm.S > 0) {
+        const void* sh[] = {Ws1, bs1, Ws2, bs2};
+        for (const void* p : sh) if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+        if (scaled && (!Ws1_scales || !Ws2_scales || !aligned16(Ws1_scales) || !aligned16(Ws2_scales)))
+            return MOE_ERR_INVALID_ARG;
+    }
+    const FewArgs a{x, W_r, logit_bias, W1, W1_scales, b1, W2, W2_scales, b2, Ws1, Ws1_scales, bs1,
+                    Ws2, Ws2_scales, bs2, out, f, P, loss, topk_idx, gates, counts};
+    return cuda_status(launch_few(dm, a, ws, static_cast<cudaStream_t>(stream)));
 }
 
 // elements of a (rows, cols) matrix, or -1 where the quantiser's grid or a
