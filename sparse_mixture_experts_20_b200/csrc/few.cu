@@ -2,14 +2,13 @@
 //
 // Decoding a few tokens is bound by the bytes of the experts they reach, so
 // the kernel is a stream of weight rows through every SM that nothing
-// interrupts: a producer warp loads 128-byte-wide pieces of weight rows by TMA
-// into a ring in shared memory, and eight consumer warps multiply them with
-// mma.sync (weights as the 16-row operand, tokens as the 8 columns; tcgen05's
-// 128-row tiles would leave most SMs without a tile, and the few tokens cost
-// nothing extra on the 8-column shape).  One block per SM, launched
-// cooperatively; the phases are separated by grid barriers, and since weights
-// do not depend on what the barriers wait for, the ring keeps filling across
-// them:
+// interrupts: a warp loads pieces of up to 128 weight rows x 128 bytes by TMA
+// into a ring in shared memory, and tcgen05 multiplies them in place, the
+// weights as the 128-row operand and the tokens as a narrow one.  No thread
+// touches a weight; what the other warps do per piece is a few copies of the
+// token side.  One block per SM, launched cooperatively; the phases are
+// separated by grid barriers, and since weights do not depend on what the
+// barriers wait for, the ring keeps filling across them:
 //   1  router logits: (expert, slice of d) dot products in fp32, partial sums
 //      per slice; x into the operand form of the weights' type;
 //   -- barrier; every block then selects the top-K of all tokens for itself
@@ -17,20 +16,30 @@
 //      an equal share of their rows, 16 at a time:
 //   2  h = SiLU(W1 x + b1), written per (token, slot);
 //   -- barrier; FP8 and MXFP4: h into the operand form, barrier;
-//   3  an equal share of the output rows: sum over the experts of
-//      gate * (W2 h + b2), shared experts included, written once as bf16.
-// The eight warps split K; their accumulators are added in warp order through
-// shared memory, once per job in phase 2 and once in phase 3.  Columns are the
-// tokens themselves: a token that did not choose the expert has a zero column.
+//   3  out = sum over the experts of gate * (W2 h + b2), shared experts
+//      included.  The output rows are cut into groups of at most 128 and, to
+//      keep groups near that size (the tensor core reads 128 rows whatever the
+//      job has), the pieces of a group's experts are dealt to `split` blocks;
+//      the last of them to finish adds the partial sums in block order.
 //
-// Operand forms (the products inside an MMA are exact, sums fp32):
-//   bf16   weights, x and h in bf16;
-//   FP8    e4m3 codes converted to fp16 (exact); x and h quantised to e4m3 per
-//          128 columns, scales applied in fp32 per 64 columns of K;
-//   MXFP4  E2M1 codes converted to fp16 (exact), the weight scale applied in
-//          fp32 per block of 32; x and h in fp16 with a power-of-two scale per
-//          128 columns, which brings their largest magnitude to 2^14..2^15:
-//          bf16 values stay exact down to 2^-29 of it, and h keeps 11 bits.
+// Operand forms (products exact, sums in fp32):
+//   bf16   weights, x and h in bf16 (kind::f16);
+//   FP8    e4m3 (kind::mxf8f6f4.block_scale); x and h quantised to e4m3 per 128
+//          columns; all scales are powers of two and go to the tensor core;
+//   MXFP4  packed E2M1 with its E8M0 scales (kind::mxf4.block_scale).  x and h
+//          are not quantised: per 32 columns they are split into five E2M1
+//          planes, each the nearest E2M1 value of what the planes before it
+//          left, at scales s, s/4, s/32, s/256, s/2048.  A plane's remainder is
+//          at most half of the step at its largest magnitude (1, then 1/2 of
+//          the next plane's unit), so the five stand for the value to within
+//          s / 4096 <= amax / 12288.  A token is then five columns, which the
+//          tensor core has to spare.
+//
+// Per block (320 threads):
+//   warps 0..3  epilogue (thread = row);   warps 4..7  token side: operand
+//   rows and all scales by cp.async, LAG pieces ahead;   (both: phase 1, the
+//   selection and the conversion of h)     warp 8  weights by TMA;
+//   warp 9  MMA issue.
 // Every wait is bounded (common.cuh); after a wait gives up, the warps skip
 // the remaining work but keep meeting at the block's barriers.
 #include <cuda.h>
@@ -42,34 +51,38 @@
 namespace moe {
 namespace {
 
-constexpr int CW = 8;                          // consumer warps
-constexpr int CT = CW * 32;                    // consumer threads
-constexpr int THREADS = CT + 32;               // + the producer warp
-constexpr int SLOTS = 10, SLOT_BYTES = 16384;  // ring
-constexpr int SCALE_BYTES = 1024;              // MXFP4: 8 scale bytes for each row of a slot
-constexpr int RED_PITCH = 132;                 // floats per column of the reduction buffer (bank spread)
+constexpr int CW = 8;                          // general warps
+constexpr int CT = CW * 32;
+constexpr int W_TMA = 8, W_MMA = 9;
+constexpr int THREADS = CT + 64;
+constexpr int EPI = 128;                       // epilogue threads, and token-side threads
+constexpr int MAX_SLOTS = 11, PIECE_BYTES = 16384;
+constexpr int LAG = 4;                         // pieces of the token side in flight
 constexpr int MAX_T = MOE_FEW_MAX_TOKENS;
+constexpr int MAX_BLOCKS = 256, MAX_SPLIT = 8;
+constexpr int PLANES = 5;                      // MXFP4: columns per token
+constexpr uint32_t ACC_COLS = 96, SF_COL0 = 2 * ACC_COLS, SF_SLOTS = 4, SF_COLS = 16, TMEM_COLS = 256;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
-constexpr int OFF_RING = 0;
-constexpr int OFF_SCALES = OFF_RING + SLOTS * SLOT_BYTES;
-constexpr int OFF_RED = OFF_SCALES + SLOTS * SCALE_BYTES;
-constexpr int OFF_IDX = OFF_RED + CW * 8 * RED_PITCH * 4;      // [16][16] int
+constexpr int OFF_IDX = 0;                                     // [16][16] int
 constexpr int OFF_GATE = OFF_IDX + MAX_T * 16 * 4;             // [16][16] float
 constexpr int OFF_MASK = OFF_GATE + MAX_T * 16 * 4;            // [256] tokens kept, per expert
 constexpr int OFF_KPACK = OFF_MASK + 256 * 4;                  // [256] 4 bits per token: its slot
 constexpr int OFF_ACT = OFF_KPACK + 256 * 8;                   // [256] experts reached, ascending
-constexpr int OFF_BAR = OFF_ACT + 256 * 4;                     // full, empty [SLOTS]
-constexpr int OFF_MISC = OFF_BAR + 2 * SLOTS * 8;              // abort flag, n_active, 8 warp counts
-constexpr int SMEM_BYTES = OFF_MISC + 64;
-constexpr int SMEM_ALLOC = SMEM_BYTES + 1024;
+constexpr int OFF_OUT = OFF_ACT + 256 * 4;                     // [16][128] fp32 output sums
+constexpr int OFF_BAR = OFF_OUT + MAX_T * 128 * 4;             // full, empty [MAX_SLOTS]; accf, acce [2]; drain
+constexpr int OFF_MISC = OFF_BAR + (2 * MAX_SLOTS + 5) * 8;    // abort flag, n_active, tmem address, last flag, 8 warp counts
+constexpr int OFF_RING = (OFF_MISC + 64 + 1023) & ~1023;
+constexpr int RING_BYTES = 208 * 1024;
+constexpr int SMEM_ALLOC = OFF_RING + RING_BYTES + 1024;
 static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
-static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0 && OFF_RED % 16 == 0, "alignment");
-static_assert(CW * 8 * RED_PITCH * 4 >= MAX_T * 256 * 4 + 256 * 4, "the router's probabilities fit the buffer");
+static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
+static_assert(RING_BYTES >= MAX_T * 256 * 4 + 256 * 4, "the router's probabilities fit the ring's memory");
+static_assert(SF_COL0 + SF_SLOTS * SF_COLS <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
 
 // grid-wide counters in the workspace, zero between launches
-enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_WORDS = 5 };
+enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_WORDS = 5, CTR_GROUP = 64 };
 
 struct __align__(64) FewParams {
     CUtensorMap w1, w2, ws1, ws2;
@@ -88,40 +101,44 @@ struct __align__(64) FewParams {
     uint32_t* ctr;
     float* part;                  // (ks, T, E) partial logits
     uint8_t* xq;                  // x in operand form (bf16: x itself)
-    float* xs;                    // (T, d / 128) its scales
+    uint8_t* xs;                  // its scales: FP8 a word per 128 columns, MXFP4 a byte per 32
     float* h32;                   // fp32 h: (T K, dff), then (S T, dffs)
-    uint8_t* hq;                  // h in operand form, same rows
-    float* hs;                    // its scales per 128
+    uint8_t* hq;                  // h in operand form, same rows (bf16: the only form)
+    uint8_t* hs;                  // its scales
+    float* sums;                  // (blocks, T, 128) partial output sums
     float alpha;
     int T, d, E, K, dff, S, dffs, capacity, slot_major, passthrough;
     int ks, slice;                // router slices of d and their length
-    int rows3;                    // output rows of a phase-3 job (the W2 maps' box)
+    int groups, split;            // phase 3: row groups, blocks per group
+    int rows3;                    // rows of a phase-3 job (the W2 maps' box)
+    int slots, slot_bytes;        // ring
 };
 
 enum { M_BF16 = 0, M_FP8 = 1, M_FP4 = 2 };
 
+// KP: elements of K in a piece (128 bytes of a weight row); P: columns per
+// token; SF: bytes of scales per slot (weights', then tokens')
 template <int MODE> struct Form;
-// K elements in 64 bytes of a weight row (a warp's half of a 128-byte piece);
-// bytes of an operand element of x and h
-template <> struct Form<M_BF16> { static constexpr int KH = 32, BB = 2; };
-template <> struct Form<M_FP8> { static constexpr int KH = 64, BB = 1; };
-template <> struct Form<M_FP4> { static constexpr int KH = 128, BB = 2; };
+template <> struct Form<M_BF16> { static constexpr int KP = 64, P = 1, SF = 0; };
+template <> struct Form<M_FP8> { static constexpr int KP = 128, P = 1, SF = 1024; };
+template <> struct Form<M_FP4> { static constexpr int KP = 256, P = PLANES, SF = 2048; };
+
+__host__ __device__ constexpr int round16(int v) { return (v + 15) & ~15; }
 
 __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); }
 
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(bar)), "r"(n) : "memory");
-}
+__device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 2, %0;" :: "n"(EPI) : "memory"); }
 
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Arrives on bar once this thread's earlier cp.async copies have landed (the
-// barrier's count includes the arrival).
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     uint32_t v;
@@ -129,57 +146,51 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     return v;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four e4m3 codes to two pairs of fp16 (exact).
-__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(codes));
-}
-
 // ---------------------------------------------------------------- operand form of x and h
 
-// 128 values, four per lane, into the operand form: codes and one scale.
+// 128 consecutive values of row `row` (a token of x, a slot of h) starting at
+// column col, four per lane, into the operand form of rows of k columns.
 template <int MODE>
-__device__ __forceinline__ void store_block(const float (&v)[4], uint8_t* dst, float* scale, int lane) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    m = __reduce_max_sync(0xffffffffu, m);
+__device__ __forceinline__ void store_block(float (&v)[4], uint8_t* q, uint8_t* scales, size_t row, int k, int col,
+                                            int lane) {
     if (MODE == M_FP8) {
-        // fmaxf semantics of the dispatch quantiser: a NaN does not count
+        // as the dispatch quantiser: fmaxf does not count a NaN
         float a = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) a = fmaxf(a, fabsf(v[j]));
-        m = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
         const float sc = pow2_scale_448(__uint_as_float(m)), inv = inv_pow2(sc);
         const uint32_t lo = f32x2_to_e4m3x2(v[0] * inv, v[1] * inv), hi = f32x2_to_e4m3x2(v[2] * inv, v[3] * inv);
-        reinterpret_cast<uint32_t*>(dst)[lane] = lo | (hi << 16);
-        if (lane == 0) *scale = sc;
+        reinterpret_cast<uint32_t*>(q + row * k + col)[lane] = lo | (hi << 16);
+        // the scale's UE8M0 byte, once per 32 columns
+        if (lane == 0) reinterpret_cast<uint32_t*>(scales)[row * (k / 128) + col / 128] =
+            (__float_as_uint(sc) >> 23) * 0x01010101u;
     } else {
-        // scale 2^k, k = exponent - 14, at least -126 (an infinity or a NaN
-        // takes the largest and stays what it is)
-        const int k = max(static_cast<int>(m >> 23) - 127 - 14, -126);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-        const __half2 a = __floats2half2_rn(v[0] * inv, v[1] * inv), b = __floats2half2_rn(v[2] * inv, v[3] * inv);
-        reinterpret_cast<uint2*>(dst)[lane] = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                                         *reinterpret_cast<const uint32_t*>(&b));
-        if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+        // eight lanes have a block of 32
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const uint32_t b = mxfp4_scale_byte(m);
+        const float inv = mxfp4_inv_scale(b == 255u ? 127u : b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= inv;
+#pragma unroll
+        for (int pl = 0; pl < PLANES; ++pl) {
+            // scale exponents b, b - 2, b - 5, b - 8, b - 11; a plane below the
+            // smallest scale holds nothing
+            const int e = static_cast<int>(b) - (pl == 0 ? 0 : 3 * pl - 1);
+            const uint32_t codes = b == 255u || e < 0 ? 0u : f32x4_to_e2m1x4(v[0], v[1], v[2], v[3]);
+            float back[4];
+            e2m1x4_to_f32(codes, back);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = (v[j] - back[j]) * (pl == 0 ? 4.f : 8.f);
+            const size_t r = row * PLANES + pl;
+            reinterpret_cast<uint16_t*>(q + (r * k + col) / 2)[lane] = static_cast<uint16_t>(codes);
+            if ((lane & 7) == 0)
+                scales[(r * k + col) / 32 + lane / 8] = static_cast<uint8_t>(b == 255u ? 255 : max(e, 0));
+        }
     }
 }
 
@@ -221,362 +232,368 @@ __device__ void grid_barrier(const Ctx& c, int which) {
 
 // ---------------------------------------------------------------- jobs
 
-// A job: `rows` consecutive rows of one matrix, streamed over all of K in
-// 128-byte pieces; a slot of the ring holds nk pieces (rows padded to
-// 128 / nk).
+// A job: `rows` (at most 128) consecutive rows of one matrix, streamed over
+// pieces p0 .. p1 - 1 of K (128 bytes of every row each), for the tokens of
+// `mask`; the j-th of them has the columns j P .. j P + P - 1.
 struct Job {
     int shared;           // 1: shared expert
     int mat, row0, rows;
     int n, k;             // the matrix: n rows of k columns
-    int nk, pieces, slots;
-    uint32_t mask;        // tokens that go through it
-    uint64_t kpack;       // routed: their slots
+    int p0, p1;
+    uint32_t mask;
+    uint64_t kpack;       // routed: the tokens' slots
 };
 
-template <int MODE>
-__device__ __forceinline__ void finish_job(Job& j, int pad_rows) {
-    j.nk = pad_rows > 64 ? 1 : pad_rows > 32 ? 2 : pad_rows > 16 ? 4 : 8;
-    j.pieces = (j.k + 2 * Form<MODE>::KH - 1) / (2 * Form<MODE>::KH);
-    j.slots = (j.pieces + j.nk - 1) / j.nk;
+__device__ __forceinline__ void set_matrix(const Ctx& c, Job& j, bool shared, int m) {
+    j.shared = shared;
+    j.mat = shared ? m : reinterpret_cast<const int*>(c.smem + OFF_ACT)[m];
+    j.mask = shared ? (1u << c.p.T) - 1u : reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK)[j.mat];
+    j.kpack = shared ? 0 : reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK)[j.mat];
+}
+
+// Row of the operand arrays of x (phase 2) or h (phase 3) for token t.
+template <int PHASE>
+__device__ __forceinline__ int token_row(const Ctx& c, const Job& j, int t) {
+    if (PHASE == 2) return t;
+    return j.shared ? j.mat * c.p.T + t : t * c.p.K + (static_cast<int>(j.kpack >> (4 * t)) & 15);
 }
 
 // Phase 2: this block's share of the rows of W1, in units of 16.
-template <int MODE, typename F>
-__device__ __forceinline__ void for_jobs2(const Ctx& c, int n_active, F&& body) {
-    const FewParams& p = c.p;
-    const uint32_t* mask = reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK);
-    const uint64_t* kpack = reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK);
-    const int* act = reinterpret_cast<const int*>(c.smem + OFF_ACT);
-    const int us = p.dffs / 16, ur = p.dff / 16;
-    const int n_shared = p.S * us;
-    const long long units = n_shared + static_cast<long long>(n_active) * ur;
-    int u = static_cast<int>(units * blockIdx.x / gridDim.x);
-    const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
-    while (u < end) {
-        Job j;
+template <int MODE>
+struct Jobs2 {
+    const Ctx& c;
+    int u, end, n_shared;
+    __device__ __forceinline__ Jobs2(const Ctx& c_, int n_active) : c(c_) {
+        const FewParams& p = c.p;
+        n_shared = p.S * (p.dffs / 16);
+        const long long units = n_shared + static_cast<long long>(n_active) * (p.dff / 16);
+        u = static_cast<int>(units * blockIdx.x / gridDim.x);
+        end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    }
+    __device__ __forceinline__ bool next(Job& j) {
+        if (u >= end) return false;
+        const FewParams& p = c.p;
         const bool sh = u < n_shared;
-        const int v = sh ? u : u - n_shared, per = sh ? us : ur;
+        const int v = sh ? u : u - n_shared, per = sh ? p.dffs / 16 : p.dff / 16;
         const int m = v / per, r = v % per;
         const int run = min(end - u, per - r);
         const int cuts = (run + 7) / 8, take = (run + cuts - 1) / cuts;
-        j.shared = sh;
-        j.mat = sh ? m : act[m];
-        j.mask = sh ? (1u << p.T) - 1u : mask[j.mat];
-        j.kpack = sh ? 0 : kpack[j.mat];
+        set_matrix(c, j, sh, m);
         j.row0 = 16 * r;
         j.rows = 16 * take;
         j.n = sh ? p.dffs : p.dff;
         j.k = p.d;
-        finish_job<MODE>(j, j.rows);
-        body(j);
+        j.p0 = 0;
+        j.p1 = (p.d + Form<MODE>::KP - 1) / Form<MODE>::KP;
         u += take;
+        return true;
     }
-}
+};
 
-// Phase 3: the matrices whose products sum into one range of output rows.
-template <int MODE, typename F>
-__device__ __forceinline__ void for_jobs3(const Ctx& c, int n_active, int row0, int rows, F&& body) {
-    const FewParams& p = c.p;
-    const uint32_t* mask = reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK);
-    const uint64_t* kpack = reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK);
-    const int* act = reinterpret_cast<const int*>(c.smem + OFF_ACT);
-    for (int m = 0; m < p.S + n_active; ++m) {
-        Job j;
-        j.shared = m < p.S;
-        j.mat = j.shared ? m : act[m - p.S];
-        j.mask = j.shared ? (1u << p.T) - 1u : mask[j.mat];
-        j.kpack = j.shared ? 0 : kpack[j.mat];
+// Phase 3: this block's share of the pieces that sum into rows row0 .. of the
+// output: the shared experts', then those of the experts reached.
+template <int MODE>
+struct Jobs3 {
+    const Ctx& c;
+    int row0, rows, at, end, ps, pr;
+    __device__ __forceinline__ Jobs3(const Ctx& c_, int n_active, int row0_, int rows_) : c(c_), row0(row0_), rows(rows_) {
+        const FewParams& p = c.p;
+        ps = (p.dffs + Form<MODE>::KP - 1) / Form<MODE>::KP;
+        pr = (p.dff + Form<MODE>::KP - 1) / Form<MODE>::KP;
+        const long long all = p.S * ps + static_cast<long long>(n_active) * pr;
+        const int s = blockIdx.x % p.split;
+        at = static_cast<int>(all * s / p.split);
+        end = static_cast<int>(all * (s + 1) / p.split);
+    }
+    __device__ __forceinline__ bool next(Job& j) {
+        if (at >= end) return false;
+        const FewParams& p = c.p;
+        const bool sh = at < p.S * ps;
+        const int v = sh ? at : at - p.S * ps, per = sh ? ps : pr;
+        const int m = v / per, first = v % per;
+        set_matrix(c, j, sh, m);
         j.row0 = row0;
         j.rows = rows;
         j.n = p.d;
-        j.k = j.shared ? p.dffs : p.dff;
-        finish_job<MODE>(j, p.rows3);
-        body(j);
+        j.k = sh ? p.dffs : p.dff;
+        j.p0 = first;
+        j.p1 = min(per, first + end - at);
+        at += j.p1 - j.p0;
+        return true;
     }
+};
+
+// The row ranges of phase 3 of this block, one after the other: body(row0, rows).
+template <typename F>
+__device__ __forceinline__ void for_rows3(const Ctx& c, F&& body) {
+    const FewParams& p = c.p;
+    const int g = blockIdx.x / p.split;
+    if (g >= p.groups) return;
+    const int begin = static_cast<int>(static_cast<long long>(p.d) * g / p.groups);
+    const int end = static_cast<int>(static_cast<long long>(p.d) * (g + 1) / p.groups);
+    for (int r = begin; r < end; r += p.rows3) body(r, min(p.rows3, end - r));
 }
 
-// ---------------------------------------------------------------- producer
-
+// A slot of the ring: the weights' piece, the tokens' rows, the scales.
 struct Ring {
     int slot = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void next() { if (++slot == SLOTS) { slot = 0; phase ^= 1u; } }
+    __device__ __forceinline__ void next(int slots) { if (++slot == slots) { slot = 0; phase ^= 1u; } }
 };
 
-// Loads every slot of a job; false after a wait gave up.  box: rows of the
-// tensor map's box (16 in phase 2; the whole job in phase 3).
+__device__ __forceinline__ uint8_t* slot_at(const Ctx& c, int slot) { return c.smem + OFF_RING + slot * c.p.slot_bytes; }
+
 template <int MODE>
-__device__ __forceinline__ bool produce(const Ctx& c, const Job& j, const CUtensorMap* map, const uint8_t* scales,
-                                        int box, Ring& ring, int& issued) {
+__device__ __forceinline__ int scales_at(const Ctx& c) { return c.p.slot_bytes - Form<MODE>::SF; }
+
+// ---------------------------------------------------------------- weights (one warp)
+
+// Loads a job's weights; false after a wait gave up.  box: rows of the tensor
+// map's box (16 in phase 2, rows3 in phase 3).
+template <int MODE>
+__device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const CUtensorMap* map, int box, Ring& ring,
+                                             int& issued) {
     const int boxes = (j.rows + box - 1) / box;
-    const int pitch = SLOT_BYTES / j.nk, srows = 128 / j.nk;
     constexpr int ELEMS = MODE == M_BF16 ? 64 : 128;        // map elements (bf16, or bytes) per piece
-    const int kq = j.k / 32;
-    for (int s = 0; s < j.slots; ++s) {
+    for (int s = j.p0; s < j.p1; ++s) {
         uint64_t* full = c.full + ring.slot;
-        const int first = s * j.nk, np = min(j.nk, j.pieces - first);
         int ok = 1;
         if (c.lane == 0) {
             ok = mbar_wait_bounded(c.empty + ring.slot, ring.phase ^ 1u, c.abort_flag, c.p.status, kWaitNs);
-            if (ok) mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * boxes * box * 128));
+            if (ok) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * box * 128));
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-        uint8_t* dst = c.smem + OFF_RING + ring.slot * SLOT_BYTES;
-        if (c.lane < np * boxes) {
-            const int q = c.lane / boxes, b = c.lane % boxes;
-            tma_load_3d(dst + q * pitch + b * box * 128, map, full, (first + q) * ELEMS, j.row0 + b * box, j.mat);
-        }
-        if (MODE == M_FP4) {
-            // the 8 scale bytes of each row of each piece, as two words
-            uint8_t* sdst = c.smem + OFF_SCALES + ring.slot * SCALE_BYTES;
-            for (int i = c.lane; i < np * srows * 2; i += 32) {
-                const int q = i / (2 * srows), r = (i >> 1) % srows, k0 = (first + q) * 8 + (i & 1) * 4;
-                if (r < j.rows && j.row0 + r < j.n && k0 < kq)
-                    cp_async_4(sdst + q * srows * 8 + r * 8 + (i & 1) * 4,
-                               scales + (static_cast<size_t>(j.mat) * j.n + j.row0 + r) * kq + k0);
-            }
-            cp_async_arrive(full);
-        }
+        if (c.lane < boxes)
+            tma_load_3d(slot_at(c, ring.slot) + c.lane * box * 128, map, full, s * ELEMS, j.row0 + c.lane * box, j.mat);
         ++issued;
-        ring.next();
+        ring.next(c.p.slots);
     }
     return true;
 }
 
-// ---------------------------------------------------------------- consumer
+// ---------------------------------------------------------------- token side (128 threads)
 
-template <int MODE, int NT>
-struct BRegs {
-    static constexpr int V = MODE == M_FP4 ? 4 : 1;        // 16-byte vectors per token column
-    uint4 v[NT][V];
-    float cs[NT][2];                                        // factors of this lane's two result columns
-    float rs[2];                                            // FP8: weight scales of the job's two row blocks
-};
-
-// What the consumers need to find the token side of a job.
-struct TokenSide {
-    const uint8_t* base;  // operand rows
-    const float* scales;  // per 128 columns, or nullptr (bf16)
-    int per_slot;         // 1: row (t, slot) of routed h; 0: row t
-    bool gated;           // multiply by the gate (phase 3, routed)
-};
-
-template <int MODE, int NT>
-__device__ __forceinline__ void load_b(const Ctx& c, const Job& j, const TokenSide& ts, const void* wscales,
-                                       int piece, BRegs<MODE, NT>& r) {
-    const int g = c.lane >> 2, t4 = c.lane & 3;
-    const int k0 = (2 * piece + (c.warp & 1)) * Form<MODE>::KH;
-    const bool in = k0 < j.k;
-    const float* gate = reinterpret_cast<const float*>(c.smem + OFF_GATE);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int t = nt * 8 + g;
-        const bool on = in && (j.mask >> t & 1u);
-        const int slot = static_cast<int>(j.kpack >> (4 * t)) & 15;
-        const size_t row = ts.per_slot ? static_cast<size_t>(t) * c.p.K + slot : t;
-        const uint8_t* src = ts.base + (row * j.k + k0) * Form<MODE>::BB;
-#pragma unroll
-        for (int b = 0; b < BRegs<MODE, NT>::V; ++b)
-            r.v[nt][b] = on ? __ldcg(reinterpret_cast<const uint4*>(src) + 4 * b + t4) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int tc = nt * 8 + 2 * t4 + i;
-            const int sc = static_cast<int>(j.kpack >> (4 * tc)) & 15;
-            float f = 0.f;
-            if (in && (j.mask >> tc & 1u)) {
-                const size_t rc = ts.per_slot ? static_cast<size_t>(tc) * c.p.K + sc : tc;
-                f = MODE == M_BF16 ? 1.f : __ldcg(ts.scales + rc * (j.k / 128) + k0 / 128);
-                if (ts.gated) f *= gate[tc * 16 + sc];
-            }
-            r.cs[nt][i] = f;
-        }
-    }
-    if (MODE == M_FP8) {
-        const float* w = static_cast<const float*>(wscales);
-        const int nb = j.n / 128, kb = j.k / 128, b0 = j.row0 / 128;
-        const float* q = w + (static_cast<size_t>(j.mat) * nb + b0) * kb + k0 / 128;
-        r.rs[0] = in ? __ldg(q) : 0.f;
-        r.rs[1] = in && b0 + 1 < nb ? __ldg(q + kb) : 0.f;
-    }
-}
-
-// acc += v * cs * rs, except in the column of a token that does not go through
-// the job (cs = 0): what an infinite or NaN weight makes of its zero operand
-// must not reach it.
-__device__ __forceinline__ void scaled_add(float& acc, float v, float cs, float rs) {
-    if (cs != 0.f) acc = fmaf(v, cs * rs, acc);
-}
-
-// One piece's half (64 bytes of every row): acc += W x for the job's rows.
-template <int MODE, int NT>
-__device__ __forceinline__ void multiply(const Ctx& c, const Job& j, const uint8_t* piece, const uint8_t* scales,
-                                         const BRegs<MODE, NT>& b, float (&acc)[8][NT][4]) {
-    const int g = c.lane >> 2, t4 = c.lane & 3, half = c.warp & 1;
-    const bool hi = NT == 2 && (j.mask >> 8) != 0;          // any token in the second column tile
-    if (MODE == M_BF16 || MODE == M_FP8) {
-        uint32_t bf[NT][8];
+// The tokens' operand rows and the scales of every piece of a phase's jobs, a
+// cp.async group per piece; a slot's arrival follows LAG pieces later, when
+// its group has landed.
+template <int MODE, int PHASE, typename Jobs>
+__device__ __forceinline__ void load_tokens(const Ctx& c, Jobs&& jobs, const uint8_t* base, const uint8_t* bscales,
+                                            int shared_row, int routed_k, const void* ws, const void* ws_shared,
+                                            Ring& ring, bool& ok) {
+    constexpr int P = Form<MODE>::P, KP = Form<MODE>::KP;
+    constexpr int NB = P;                                      // operand rows a thread copies: 16 at a time, 16 P in all
+    const int i = c.tid - EPI;
+    const int q = i & 7;                                       // 16-byte chunk of a row's 128 bytes
+    const int word = 16 * (i & 31) + 4 * (i >> 5);             // row i's word in 512 bytes of scales
+    Ring done = ring;
+    int pending = 0;
+    auto arrive = [&]() {
         if (MODE == M_FP8) {
+            // the weight scale arrived as fp32: its UE8M0 byte, once per 32 columns
+            uint32_t* w = reinterpret_cast<uint32_t*>(slot_at(c, done.slot) + scales_at<MODE>(c) + word);
+            *w = ((*w >> 23) & 0xFFu) * 0x01010101u;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive(c.full + done.slot);
+        done.next(c.p.slots);
+    };
+    Job j;
+    while (ok && jobs.next(j)) {
+        const int rows = __popc(j.mask) * P;
+        // bytes of an operand row of j.k columns
+        const size_t pitch = MODE == M_BF16 ? 2 * static_cast<size_t>(j.k) : MODE == M_FP8 ? j.k : j.k / 2;
+        // shared experts' rows of h follow the routed ones, at their own width
+        const uint8_t* data = base;
+        const uint8_t* sc = bscales;
+        if (PHASE == 3 && j.shared) {
+            const size_t skip = static_cast<size_t>(shared_row) * P * routed_k;     // elements
+            data += MODE == M_BF16 ? 2 * skip : MODE == M_FP8 ? skip : skip / 2;
+            sc += MODE == M_FP8 ? skip / 128 * 4 : skip / 32;
+        }
+        auto operand_row = [&](int n) {                        // of column n
+            uint32_t m = j.mask;
+            for (int z = n / P; z > 0; --z) m &= m - 1;
+            return token_row<PHASE>(c, j, __ffs(m) - 1) * P + n % P;
+        };
+        const uint8_t* src[NB];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t w[4] = {b.v[nt][0].x, b.v[nt][0].y, b.v[nt][0].z, b.v[nt][0].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) e4m3x4_to_f16x2(w[q], bf[nt][2 * q], bf[nt][2 * q + 1]);
+        for (int b = 0; b < NB; ++b) {
+            const int n = (i >> 3) + 16 * b;
+            src[b] = n < rows ? data + operand_row(n) * pitch + 16 * q : nullptr;
+        }
+        const uint8_t* bs = nullptr;                           // scales of column i
+        const uint8_t* as = nullptr;                           // scales of weight row i
+        const int kq = MODE == M_FP8 ? j.k / 128 * 4 : j.k / 32;
+        if (MODE != M_BF16) {
+            if (i < rows) bs = sc + static_cast<size_t>(operand_row(i)) * kq;
+            if (i < j.rows && j.row0 + i < j.n) {
+                const uint8_t* w = static_cast<const uint8_t*>(j.shared ? ws_shared : ws);
+                as = MODE == M_FP8 ? w + (static_cast<size_t>(j.mat) * (j.n / 128) + (j.row0 + i) / 128) * kq
+                                   : w + (static_cast<size_t>(j.mat) * j.n + j.row0 + i) * kq;
             }
         }
-        const int split = (j.row0 / 128 + 1) * 128 - j.row0;   // first row of the second scale block
+        for (int s = j.p0; s < j.p1; ++s) {
+            int w = 1;
+            if (c.lane == 0) w = mbar_wait_bounded(c.empty + ring.slot, ring.phase ^ 1u, c.abort_flag, c.p.status, kWaitNs);
+            if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+            uint8_t* slot = slot_at(c, ring.slot);
+            uint8_t* bdst = slot + PIECE_BYTES;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            if (16 * m >= j.rows) break;
-            const int r0 = 16 * m + g;
-            // 16-byte chunk q of row r is at chunk q ^ (r mod 8) (128-byte swizzle); r0 and r0 + 8 swizzle alike
-            const uint32_t off = static_cast<uint32_t>(r0 * 128 + (((half * 4 + t4) ^ g) << 4));
-            const uint4 w0 = *reinterpret_cast<const uint4*>(piece + off);
-            const uint4 w1 = *reinterpret_cast<const uint4*>(piece + off + 8 * 128);
-            const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
-            float s[NT][4] = {};
-            if (MODE == M_BF16) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t bw[4] = {b.v[nt][0].x, b.v[nt][0].y, b.v[nt][0].z, b.v[nt][0].w};
-                        if (nt == 0 || hi)
-                            mma_bf16(s[nt], a0[2 * q], a1[2 * q], a0[2 * q + 1], a1[2 * q + 1], bw[2 * q], bw[2 * q + 1]);
-                    }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) scaled_add(acc[m][nt][i], s[nt][i], b.cs[nt][i & 1], 1.f);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t f0, f1, f2, f3;
-                    e4m3x4_to_f16x2(a0[q], f0, f2);
-                    e4m3x4_to_f16x2(a1[q], f1, f3);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt == 0 || hi) mma_f16(s[nt], f0, f1, f2, f3, bf[nt][2 * q], bf[nt][2 * q + 1]);
-                }
-                const float rs0 = r0 < split ? b.rs[0] : b.rs[1], rs1 = r0 + 8 < split ? b.rs[0] : b.rs[1];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        scaled_add(acc[m][nt][i], s[nt][i], b.cs[nt][i & 1], i < 2 ? rs0 : rs1);
+            for (int b = 0; b < NB; ++b) {
+                const int n = (i >> 3) + 16 * b;
+                if (src[b] && (MODE != M_FP4 || static_cast<size_t>(s) * 128 + 16 * q < pitch))
+                    cp_async_16(bdst + n * 128 + ((q ^ (n & 7)) << 4), src[b] + static_cast<size_t>(s) * 128);
             }
+            if (MODE != M_BF16) {
+                uint8_t* sf = slot + scales_at<MODE>(c) + word;
+                if (MODE == M_FP8) {
+                    if (as) cp_async_4(sf, as + 4 * s);
+                    if (bs) cp_async_4(sf + 512, bs + 4 * s);
+                } else {
+                    const bool two = s * KP + 128 < j.k;       // the piece's second 128 columns exist
+                    if (as) {
+                        cp_async_4(sf, as + 8 * s);
+                        if (two) cp_async_4(sf + 512, as + 8 * s + 4);
+                    }
+                    if (bs) {
+                        cp_async_4(sf + 1024, bs + 8 * s);
+                        if (two) cp_async_4(sf + 1536, bs + 8 * s + 4);
+                    }
+                }
+            }
+            cp_async_commit();
+            ring.next(c.p.slots);
+            if (++pending > LAG) {
+                cp_async_wait<LAG>();
+                arrive();
+                --pending;
+            }
+        }
+    }
+    cp_async_wait<0>();
+    for (; pending > 0; --pending) arrive();
+}
+
+// ---------------------------------------------------------------- MMA issue (one thread)
+
+struct MmaState {
+    Ring ring;
+    int jobs = 0, pieces = 0;
+    bool issued = false;
+};
+
+template <int MODE>
+__device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, uint32_t tmem, uint64_t* accf, uint64_t* acce,
+                                          MmaState& st) {
+    const int buf = st.jobs & 1;
+    if (!mbar_wait_bounded(acce + buf, ((st.jobs >> 1) & 1) ^ 1u, c.abort_flag, c.p.status, kWaitNs)) return false;
+    tc_fence_after();
+    const uint32_t d = tmem + buf * ACC_COLS;
+    const uint32_t n = round16(__popc(j.mask) * Form<MODE>::P);
+    uint32_t idesc;
+    if (MODE == M_BF16) idesc = make_idesc(1, 128, n);
+    else if (MODE == M_FP8) idesc = make_idesc_mxf8(128, n);
+    else idesc = 0;                                            // made per MMA below
+    for (int s = j.p0; s < j.p1; ++s) {
+        if (!mbar_wait_bounded(c.full + st.ring.slot, st.ring.phase, c.abort_flag, c.p.status, kWaitNs)) return false;
+        uint8_t* slot = slot_at(c, st.ring.slot);
+        const uint64_t a = smem_desc_k_sw128(slot), b = smem_desc_k_sw128(slot + PIECE_BYTES);
+        const uint32_t more = s > j.p0 ? 1u : 0u;
+        if (MODE == M_BF16) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, idesc, more | (k > 0));
+        } else {
+            // the MMAs that read this slot of scales SF_SLOTS pieces ago are done
+            if (st.pieces >= static_cast<int>(SF_SLOTS)) {
+                int q = st.ring.slot - static_cast<int>(SF_SLOTS);
+                uint32_t ph = st.ring.phase;
+                if (q < 0) { q += c.p.slots; ph ^= 1u; }
+                if (!mbar_wait_bounded(c.empty + q, ph, c.abort_flag, c.p.status, kWaitNs)) return false;
+            }
+            tc_fence_after();
+            const uint8_t* sf = slot + scales_at<MODE>(c);
+            const uint32_t t = tmem + SF_COL0 + (st.pieces % SF_SLOTS) * SF_COLS;
+            if (MODE == M_FP8) {
+                tmem_cp_scales(t, sf);
+                tmem_cp_scales(t + 4, sf + 512);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_mxf8_bs(d, a + 2 * k, b + 2 * k, idesc, t, t + 4, more | (k > 0));
+            } else {
+                const bool two = s * Form<MODE>::KP + 128 < j.k;
+                tmem_cp_scales(t, sf);
+                tmem_cp_scales(t + 8, sf + 1024);
+                if (two) {
+                    tmem_cp_scales(t + 4, sf + 512);
+                    tmem_cp_scales(t + 12, sf + 1536);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < 2 || two)
+                        umma_mxf4_bs(d, a + 2 * k, b + 2 * k, make_idesc_mxf4(n, 2 * (k & 1)), t + 4 * (k >> 1),
+                                  t + 8 + 4 * (k >> 1), more | (k > 0));
+            }
+        }
+        st.issued = true;
+        ++st.pieces;
+        umma_commit(c.empty + st.ring.slot);
+        st.ring.next(c.p.slots);
+    }
+    umma_commit(accf + buf);
+    ++st.jobs;
+    return true;
+}
+
+// ---------------------------------------------------------------- epilogue (128 threads, thread = row)
+
+// Waits for a job's accumulator and gives body(token, value) for every token
+// of the job, in ascending order.
+template <int MODE, typename F>
+__device__ __forceinline__ void read_job(const Ctx& c, const Job& j, uint32_t tmem, uint64_t* accf, uint64_t* acce,
+                                         int& jobs, bool& ok, F&& body) {
+    const int buf = jobs & 1;
+    if (ok) {
+        int w = 1;
+        if (c.lane == 0) w = mbar_wait_bounded(accf + buf, (jobs >> 1) & 1, c.abort_flag, c.p.status, kWaitNs);
+        ok = __shfl_sync(0xffffffffu, w, 0) != 0;
+    }
+    ++jobs;
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t acc = tmem + (static_cast<uint32_t>(c.warp * 32) << 16) + buf * ACC_COLS;
+    uint32_t m = j.mask;
+    if (Form<MODE>::P == 1) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(acc, r);
+        tmem_ld_wait_regs(r);
+        tc_fence_before();
+        mbar_arrive(acce + buf);
+#pragma unroll
+        for (int i = 0; i < MAX_T; ++i) {
+            if (!m) break;
+            body(__ffs(m) - 1, __uint_as_float(r[i]));
+            m &= m - 1;
         }
     } else {
-        // ldmatrix: matrix i holds rows 8 (i & 1) .. + 7 of block i >> 1; lane l
-        // names row l & 7 of matrix l >> 3 and receives 4 bytes of row l >> 2
-        const int lr = (c.lane & 7) + ((c.lane >> 3) & 1) * 8, lb = c.lane >> 4;
+        // five columns a token (the load reads three more)
+        for (int i = 0; m; ++i, m &= m - 1) {
+            uint32_t r[8];
+            tmem_ld_32x32b_x8(acc + static_cast<uint32_t>(PLANES * i), r);
+            tmem_ld_wait_regs(r);
+            float v = __uint_as_float(r[PLANES - 1]);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            if (16 * m >= j.rows) break;
-            const uint32_t s0 = *reinterpret_cast<const uint32_t*>(scales + (16 * m + g) * 8 + half * 4);
-            const uint32_t s1 = *reinterpret_cast<const uint32_t*>(scales + (16 * m + g + 8) * 8 + half * 4);
-            float s[NT][4] = {};
-#pragma unroll
-            for (int pr = 0; pr < 2; ++pr) {                 // two pairs of blocks
-                const int chunk = half * 4 + pr * 2 + lb;
-                const uint32_t addr = smem_u32(piece) + static_cast<uint32_t>((16 * m + lr) * 128 + ((chunk ^ (lr & 7)) << 4));
-                uint32_t w[4];
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
-#pragma unroll
-                for (int bb = 0; bb < 2; ++bb) {
-                    const int blk = pr * 2 + bb;
-                    uint32_t a0[4], a1[4];
-                    e2m1x8_to_f16x2(w[2 * bb], a0);
-                    e2m1x8_to_f16x2(w[2 * bb + 1], a1);
-                    const float rs0 = e8m0_value((s0 >> (8 * blk)) & 255u), rs1 = e8m0_value((s1 >> (8 * blk)) & 255u);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (nt && !hi) continue;
-                        const uint4 bv = b.v[nt][blk];
-                        float t[4] = {};
-                        mma_f16(t, a0[0], a1[0], a0[1], a1[1], bv.x, bv.y);
-                        mma_f16(t, a0[2], a1[2], a0[3], a1[3], bv.z, bv.w);
-                        s[nt][0] = fmaf(t[0], rs0, s[nt][0]);
-                        s[nt][1] = fmaf(t[1], rs0, s[nt][1]);
-                        s[nt][2] = fmaf(t[2], rs1, s[nt][2]);
-                        s[nt][3] = fmaf(t[3], rs1, s[nt][3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) scaled_add(acc[m][nt][i], s[nt][i], b.cs[nt][i & 1], 1.f);
+            for (int q = PLANES - 2; q >= 0; --q) v += __uint_as_float(r[q]);
+            body(__ffs(m) - 1, v);
         }
+        tc_fence_before();
+        mbar_arrive(acce + buf);
     }
-}
-
-// Streams a job's slots.  Warp w takes the pieces congruent to w / 2 modulo 4
-// and of each the half w & 1; every slot's empty barrier counts 8 arrivals
-// from the warps that have a piece in it.
-template <int MODE, int NT>
-__device__ __forceinline__ void consume(const Ctx& c, const Job& j, const TokenSide& ts, const void* wscales,
-                                        Ring& ring, bool& ok, float (&acc)[8][NT][4]) {
-    const int mine = c.warp >> 1;
-    const int pitch = SLOT_BYTES / j.nk, spitch = SCALE_BYTES / j.nk;
-    const uint32_t weight = j.nk == 1 ? 4u : j.nk == 2 ? 2u : 1u;
-    BRegs<MODE, NT> cur, nxt;
-    if (mine < j.pieces) load_b<MODE, NT>(c, j, ts, wscales, mine, cur);
-    for (int s = 0; s < j.slots; ++s, ring.next()) {
-        const int first = s * j.nk;
-        if (j.nk == 1 && (s & 3) != mine) continue;
-        if (j.nk == 2 && (s & 1) != mine >> 1) continue;
-        const int q0 = j.nk == 1 ? 0 : j.nk == 2 ? (mine & 1) : mine;
-        if (ok) {
-            int w = 1;
-            if (c.lane == 0) w = mbar_wait_bounded(c.full + ring.slot, ring.phase, c.abort_flag, c.p.status, kWaitNs);
-            ok = __shfl_sync(0xffffffffu, w, 0) != 0;
-        }
-        for (int q = q0; q < j.nk; q += 4) {
-            const int piece = first + q;
-            if (piece >= j.pieces) break;
-            if (piece + 4 < j.pieces) load_b<MODE, NT>(c, j, ts, wscales, piece + 4, nxt);
-            if (ok && (2 * piece + (c.warp & 1)) * Form<MODE>::KH < j.k)
-                multiply<MODE, NT>(c, j, c.smem + OFF_RING + ring.slot * SLOT_BYTES + q * pitch,
-                                   c.smem + OFF_SCALES + ring.slot * SCALE_BYTES + q * spitch, cur, acc);
-            cur = nxt;
-        }
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive_n(c.empty + ring.slot, weight);
-    }
-}
-
-// The sum over the warps of one column tile's accumulators, in warp order:
-// body(row, column of the tile, sum) for every row below `rows`.  Every
-// consumer thread calls it; the buffer is free again afterwards.
-template <int NT, typename F>
-__device__ __forceinline__ void reduce_tile(const Ctx& c, int nt, int rows, const float (&acc)[8][NT][4], F&& body) {
-    float* red = reinterpret_cast<float*>(c.smem + OFF_RED);
-    const int g = c.lane >> 2, t4 = c.lane & 3;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        if (16 * m >= rows) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v = acc[m][0][i];
-            if (NT == 2 && nt == 1) v = acc[m][NT - 1][i];
-            red[(c.warp * 8 + 2 * t4 + (i & 1)) * RED_PITCH + 16 * m + g + 8 * (i >> 1)] = v;
-        }
-    }
-    bar_consumers();
-    for (int i = c.tid; i < rows * 8; i += CT) {
-        const int col = i / rows, r = i % rows;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < CW; ++w) v += red[(w * 8 + col) * RED_PITCH + r];
-        body(r, col, v);
-    }
-    bar_consumers();
 }
 
 // ---------------------------------------------------------------- phase 1
 
-template <int MODE, int NT>
+template <int MODE>
 __device__ __forceinline__ void router_and_x(const Ctx& c) {
     const FewParams& p = c.p;
     if (MODE != M_BF16) {
@@ -584,10 +601,9 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
         for (int i = blockIdx.x * CW + c.warp; i < p.T * nb; i += gridDim.x * CW) {
             const int t = i / nb, b = i % nb;
             const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.d + b * 128) + c.lane);
-            const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                                __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
-            store_block<MODE>(v, p.xq + (static_cast<size_t>(t) * p.d + b * 128) * Form<MODE>::BB,
-                              p.xs + static_cast<size_t>(t) * nb + b, c.lane);
+            float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
+            store_block<MODE>(v, p.xq, p.xs, t, p.d, b * 128, c.lane);
         }
     }
     // items (slice, expert), slice-major: a block mostly stays in one slice of
@@ -608,12 +624,12 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
         bar_consumers();
         for (int e = e0 + c.warp; e < e1; e += CW) {
             const float4* w = reinterpret_cast<const float4*>(p.W_r + static_cast<size_t>(e) * p.d + k0);
-            float acc[8 * NT] = {};
+            float acc[MAX_T] = {};
 #pragma unroll 4
             for (int q = c.lane; q < len / 4; q += 32) {
                 const float4 wv = __ldg(w + q);
 #pragma unroll
-                for (int t = 0; t < 8 * NT; ++t) {
+                for (int t = 0; t < MAX_T; ++t) {
                     if (t < p.T) {
                         const uint2 xv = *reinterpret_cast<const uint2*>(xsm + t * p.slice + 4 * q);
                         acc[t] = fmaf(__uint_as_float(xv.x << 16), wv.x, acc[t]);
@@ -624,7 +640,7 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
                 }
             }
 #pragma unroll
-            for (int t = 0; t < 8 * NT; ++t) {
+            for (int t = 0; t < MAX_T; ++t) {
                 if (t >= p.T) break;
                 float v = acc[t];
 #pragma unroll
@@ -655,26 +671,29 @@ __device__ int select_experts(const Ctx& c) {
     uint64_t* kpack_s = reinterpret_cast<uint64_t*>(c.smem + OFF_KPACK);
     int* act_s = reinterpret_cast<int*>(c.smem + OFF_ACT);
     int* misc = reinterpret_cast<int*>(c.smem + OFF_MISC);
-    float* prob_s = reinterpret_cast<float*>(c.smem + OFF_RED);       // [T][256], last block only
+    float* prob_s = reinterpret_cast<float*>(c.smem + OFF_RING);      // [T][256], last block only
     const bool writer = blockIdx.x == gridDim.x - 1;
     for (int t = c.warp; t < p.T; t += CW) {
         float l[8];
         uint32_t key[8];
         float top = -INFINITY;
+        const float* part = p.part + static_cast<size_t>(t) * p.E + c.lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < p.ks; ++s) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (32 * i + c.lane < p.E) l[i] += __ldcg(part + static_cast<size_t>(s) * p.T * p.E + 32 * i);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = 32 * i + c.lane;
-            l[i] = -INFINITY;
-            key[i] = 0;
-            if (e < p.E) {
-                float v = 0.f;
-#pragma unroll 4
-                for (int s = 0; s < p.ks; ++s) v += __ldcg(p.part + (static_cast<size_t>(s) * p.T + t) * p.E + e);
-                if (p.logit_bias) v += __ldg(p.logit_bias + e);
-                l[i] = v;
-                key[i] = order_key(p.sel_bias ? v + __ldg(p.sel_bias + e) : v);
-                top = fmaxf(top, v);
-            }
+            const bool in = e < p.E;
+            if (in && p.logit_bias) l[i] += __ldg(p.logit_bias + e);
+            key[i] = in ? order_key(p.sel_bias ? l[i] + __ldg(p.sel_bias + e) : l[i]) : 0u;
+            if (!in) l[i] = -INFINITY;
+            top = fmaxf(top, l[i]);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -709,32 +728,35 @@ __device__ int select_experts(const Ctx& c) {
         }
         if (c.lane < p.K) gate_s[t * 16 + c.lane] = mine / chosen;
     }
+    mask_s[c.tid] = 0;
+    kpack_s[c.tid] = 0;
     bar_consumers();
-    // one thread per expert: its slots in capacity order
-    const int e = c.tid;
-    int count = 0, kept = 0;
-    uint32_t mask = 0;
-    uint64_t kpack = 0;
-    const int cap = p.capacity < 0 ? MAX_T : p.capacity;
-    auto slot = [&](int t, int k) {
-        if (idx_s[t * 16 + k] == e) {
-            ++count;
-            if (kept < cap) {
-                ++kept;
-                mask |= 1u << t;
-                kpack |= static_cast<uint64_t>(k) << (4 * t);
-            }
+    // the slots of every expert as bits (a token has at most one)
+    {
+        const int t = c.tid / 16, k = c.tid % 16;
+        if (t < p.T && k < p.K) {
+            const int e = idx_s[t * 16 + k];
+            atomicOr(mask_s + e, 1u << t);
+            atomicOr(reinterpret_cast<unsigned long long*>(kpack_s + e), static_cast<unsigned long long>(k) << (4 * t));
         }
-    };
-    if (p.slot_major) {
-        for (int k = 0; k < p.K; ++k)
-            for (int t = 0; t < p.T; ++t) slot(t, k);
-    } else {
-        for (int t = 0; t < p.T; ++t)
-            for (int k = 0; k < p.K; ++k) slot(t, k);
     }
-    mask_s[e] = mask;
-    kpack_s[e] = kpack;
+    bar_consumers();
+    // one thread per expert: those within the capacity
+    const int e = c.tid;
+    uint32_t mask = mask_s[e];
+    const int count = __popc(mask);
+    if (p.capacity >= 0 && count > p.capacity) {
+        uint32_t keep = 0;
+        int left = p.capacity;
+        const uint64_t kpack = kpack_s[e];
+        for (int k = 0; k < (p.slot_major ? p.K : 1); ++k)
+            for (uint32_t m = mask; m && left > 0; m &= m - 1) {
+                const int t = __ffs(m) - 1;
+                if (!p.slot_major || (static_cast<int>(kpack >> (4 * t)) & 15) == k) { keep |= 1u << t; --left; }
+            }
+        mask = keep;
+        mask_s[e] = keep;
+    }
     const uint32_t votes = __ballot_sync(0xffffffffu, mask != 0);
     if (c.lane == 0) misc[4 + c.warp] = __popc(votes);
     bar_consumers();
@@ -781,31 +803,36 @@ __device__ int select_experts(const Ctx& c) {
 
 // ---------------------------------------------------------------- the kernel
 
-template <int MODE, int NT>
+template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
 few_tokens_kernel(const __grid_constant__ FewParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t* accf = full + 2 * MAX_SLOTS;
+    uint64_t* acce = accf + 2;
+    uint64_t* drain = acce + 2;
     int* misc = reinterpret_cast<int*>(smem + OFF_MISC);
-    const Ctx c{p, smem, full, full + SLOTS, misc, static_cast<int>(threadIdx.x), static_cast<int>(threadIdx.x >> 5),
-                static_cast<int>(threadIdx.x & 31)};
+    const Ctx c{p, smem, full, full + MAX_SLOTS, misc, static_cast<int>(threadIdx.x),
+                static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31)};
     if (c.tid == 0) {
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(c.full + i, MODE == M_FP4 ? 33 : 1);      // expect_tx, and a lane each of the scale copies
-            mbar_init(c.empty + i, CW);
+        for (int i = 0; i < p.slots; ++i) {
+            mbar_init(c.full + i, 1 + 4);                       // expect_tx, the four token-side warps
+            mbar_init(c.empty + i, 1);
         }
+        for (int i = 0; i < 2; ++i) { mbar_init(accf + i, 1); mbar_init(acce + i, EPI); }
+        mbar_init(drain, 1);
         misc[0] = 0;
         fence_mbar_init();
     }
+    if (c.warp == W_MMA) tmem_alloc<TMEM_COLS>(reinterpret_cast<uint32_t*>(misc + 2));
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = static_cast<uint32_t>(misc[2]);
 
-    const int row_begin = static_cast<int>(static_cast<long long>(p.d) * blockIdx.x / gridDim.x);
-    const int row_end = static_cast<int>(static_cast<long long>(p.d) * (blockIdx.x + 1) / gridDim.x);
-
-    if (c.warp == CW) {
-        // ================= producer
+    if (c.warp == W_TMA) {
         if (c.lane == 0) {
             tma_prefetch_desc(&p.w1);
             tma_prefetch_desc(&p.w2);
@@ -816,125 +843,153 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         Ring ring;
         int issued = 0;
         bool ok = *c.abort_flag == 0;
-        for_jobs2<MODE>(c, n_active, [&](const Job& j) {
-            if (ok) ok = produce<MODE>(c, j, j.shared ? &p.ws1 : &p.w1,
-                                       static_cast<const uint8_t*>(j.shared ? p.ws1s : p.w1s), 16, ring, issued);
+        Job j;
+        for (Jobs2<MODE> jobs(c, n_active); ok && jobs.next(j);)
+            ok = load_weights<MODE>(c, j, j.shared ? &p.ws1 : &p.w1, 16, ring, issued);
+        for_rows3(c, [&](int row0, int rows) {
+            for (Jobs3<MODE> jobs(c, n_active, row0, rows); ok && jobs.next(j);)
+                ok = load_weights<MODE>(c, j, j.shared ? &p.ws2 : &p.w2, p.rows3, ring, issued);
         });
-        for (int r = row_begin; r < row_end; r += p.rows3)
-            for_jobs3<MODE>(c, n_active, r, min(p.rows3, row_end - r), [&](const Job& j) {
-                if (ok) ok = produce<MODE>(c, j, j.shared ? &p.ws2 : &p.w2,
-                                           static_cast<const uint8_t*>(j.shared ? p.ws2s : p.w2s), p.rows3, ring, issued);
-            });
-        if (MODE == M_FP4) asm volatile("cp.async.wait_all;" ::: "memory");
-        // copies in flight land before the block gives its memory back
+        // copies in flight land before the block gives its memory back (only
+        // the weights' bytes are waited for where the token side gave up: its
+        // arrivals are made good here)
+        if (!ok && c.lane == 0) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < kDrainNs) {}
+        }
+        __syncwarp();
+    } else if (c.warp == W_MMA) {
+        __syncthreads();
+        const int n_active = misc[1];
         if (c.lane == 0) {
-            int s = ring.slot;
-            uint32_t ph = ring.phase;
-            for (int i = 0; i < min(issued, SLOTS); ++i) {
-                if (--s < 0) { s = SLOTS - 1; ph ^= 1u; }
+            MmaState st;
+            bool ok = *c.abort_flag == 0;
+            Job j;
+            for (Jobs2<MODE> jobs(c, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
+            for_rows3(c, [&](int row0, int rows) {
+                for (Jobs3<MODE> jobs(c, n_active, row0, rows); ok && jobs.next(j);)
+                    ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
+            });
+            if (!ok && st.issued) {
+                umma_commit(drain);
                 volatile int no_abort = 0;
-                mbar_wait_bounded(c.full + s, ph, &no_abort, nullptr, kDrainNs);
+                mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainNs);
             }
         }
         __syncwarp();
     } else {
-        // ================= consumers
-        router_and_x<MODE, NT>(c);
+        router_and_x<MODE>(c);
         grid_barrier(c, 0);
         const int n_active = select_experts(c);
-        fence_proxy_async_smem();       // phase 1 used the ring's memory
+        fence_proxy_async_smem();                               // phase 1 and the selection used the ring's memory
         __syncthreads();
+        const int slots_h = p.T * p.K;                          // rows of routed h
+        const size_t h_shared = static_cast<size_t>(slots_h) * p.dff;
+        const bool epilogue = c.warp < 4;
+        const int my_row = c.tid;                               // epilogue: this thread's row of a job
         Ring ring;
+        int jobs_read = 0;
         bool ok = *c.abort_flag == 0;
-        float acc[8][NT][4];
-        const size_t h_shared = static_cast<size_t>(p.T) * p.K * p.dff;   // first element of the shared rows of h
-        for_jobs2<MODE>(c, n_active, [&](const Job& j) {
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.f;
-            const TokenSide ts{p.xq, p.xs, 0, false};
-            consume<MODE, NT>(c, j, ts, j.shared ? p.ws1s : p.w1s, ring, ok, acc);
-            const float* bias = (j.shared ? p.bs1 : p.b1) + static_cast<size_t>(j.mat) * j.n + j.row0;
-            const size_t base = j.shared ? h_shared + static_cast<size_t>(j.mat) * p.T * j.n : 0;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (nt && !(j.mask >> 8)) continue;
-                reduce_tile<NT>(c, nt, j.rows, acc, [&](int r, int col, float v) {
-                    const int t = nt * 8 + col;
-                    if (!(j.mask >> t & 1u)) return;
-                    const int slot = static_cast<int>(j.kpack >> (4 * t)) & 15;
-                    const size_t row = j.shared ? t : static_cast<size_t>(t) * p.K + slot;
-                    const float h = silu_fast(v + __ldg(bias + r));
-                    const size_t at = base + row * j.n + j.row0 + r;
+        Job j;
+        if (epilogue) {
+            for (Jobs2<MODE> jobs(c, n_active); jobs.next(j);) {
+                const bool in = my_row < j.rows;
+                const float bias = in ? __ldg((j.shared ? p.bs1 : p.b1) + static_cast<size_t>(j.mat) * j.n + j.row0 + my_row)
+                                      : 0.f;
+                const size_t base = j.shared ? h_shared : 0;
+                read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
+                    if (!in) return;
+                    const float h = silu_fast(v + bias);
+                    const size_t at = base + static_cast<size_t>(token_row<3>(c, j, t)) * j.n + j.row0 + my_row;
                     if (MODE == M_BF16) reinterpret_cast<__nv_bfloat16*>(p.hq)[at] = __float2bfloat16_rn(h);
                     else p.h32[at] = h;
                 });
             }
-        });
-        grid_barrier(c, 1);
-        const size_t hs_shared = h_shared / 128;
-        if (MODE != M_BF16) {
-            // a warp per 128 values of h that phase 3 reads
-            const int* idx_s = reinterpret_cast<const int*>(smem + OFF_IDX);
-            const uint32_t* mask_s = reinterpret_cast<const uint32_t*>(smem + OFF_MASK);
-            const uint64_t* kpack_s = reinterpret_cast<const uint64_t*>(smem + OFF_KPACK);
-            const int nr = p.dff / 128, ns = p.dffs / 128;
-            const int routed = p.T * p.K * nr, all = routed + p.S * p.T * ns;
-            for (int i = blockIdx.x * CW + c.warp; i < all; i += gridDim.x * CW) {
-                size_t blk;
-                if (i < routed) {
-                    const int s = i / nr, t = s / p.K, k = s % p.K, e = idx_s[t * 16 + k];
-                    // a slot over the capacity has no h
-                    if (!(mask_s[e] >> t & 1u) || (static_cast<int>(kpack_s[e] >> (4 * t)) & 15) != k) continue;
-                    blk = i;
-                } else {
-                    blk = hs_shared + (i - routed);
-                }
-                const float4 q = __ldcg(reinterpret_cast<const float4*>(p.h32 + blk * 128) + c.lane);
-                const float v[4] = {q.x, q.y, q.z, q.w};
-                store_block<MODE>(v, p.hq + blk * 128 * Form<MODE>::BB, p.hs + blk, c.lane);
-            }
-            grid_barrier(c, 2);
+        } else {
+            load_tokens<MODE, 2>(c, Jobs2<MODE>(c, n_active), p.xq, p.xs, 0, 0, p.w1s, p.ws1s, ring, ok);
         }
+        grid_barrier(c, 1);
         const int* idx_s = reinterpret_cast<const int*>(smem + OFF_IDX);
         const float* gate_s = reinterpret_cast<const float*>(smem + OFF_GATE);
         const uint32_t* mask_s = reinterpret_cast<const uint32_t*>(smem + OFF_MASK);
-        for (int r0 = row_begin; r0 < row_end; r0 += p.rows3) {
-            const int rows = min(p.rows3, row_end - r0);
-#pragma unroll
-            for (int m = 0; m < 8; ++m)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.f;
-            for_jobs3<MODE>(c, n_active, r0, rows, [&](const Job& j) {
-                const size_t at = j.shared ? h_shared + static_cast<size_t>(j.mat) * p.T * j.k : 0;
-                const TokenSide ts{p.hq + at * Form<MODE>::BB, p.hs + at / 128, !j.shared, !j.shared};
-                consume<MODE, NT>(c, j, ts, j.shared ? p.ws2s : p.w2s, ring, ok, acc);
-            });
-            ok = ok && *c.abort_flag == 0;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                reduce_tile<NT>(c, nt, rows, acc, [&](int r, int col, float v) {
-                    const int t = nt * 8 + col;
-                    if (t >= p.T || !ok) return;
-                    const int row = r0 + r;
-                    for (int k = 0; k < p.K; ++k) {
-                        const int e = idx_s[t * 16 + k];
-                        const float g = gate_s[t * 16 + k];
-                        if (mask_s[e] >> t & 1u) v = fmaf(g, __ldg(p.b2 + static_cast<size_t>(e) * p.d + row), v);
-                        else if (p.passthrough)
-                            v = fmaf(g, __bfloat162float(p.x[static_cast<size_t>(t) * p.d + row]), v);
-                    }
-                    for (int s = 0; s < p.S; ++s) v += __ldg(p.bs2 + static_cast<size_t>(s) * p.d + row);
-                    p.out[static_cast<size_t>(t) * p.d + row] = __float2bfloat16_rn(v);
-                });
+        if (MODE != M_BF16) {
+            // a warp per 128 values of h that phase 3 reads; a slot over the capacity has none
+            constexpr int P = Form<MODE>::P;
+            const int nr = p.dff / 128, ns = p.dffs / 128;
+            const int routed = slots_h * nr, all = routed + p.S * p.T * ns;
+            uint8_t* hq_shared = p.hq + h_shared * P / (MODE == M_FP4 ? 2 : 1);
+            uint8_t* hs_shared = p.hs + (MODE == M_FP4 ? h_shared * P / 32 : h_shared / 128 * 4);
+            for (int i = blockIdx.x * CW + c.warp; i < all; i += gridDim.x * CW) {
+                const bool sh = i >= routed;
+                const int u = sh ? i - routed : i, nb = sh ? ns : nr, row = u / nb, col = u % nb * 128;
+                if (!sh && !(mask_s[idx_s[row / p.K * 16 + row % p.K]] >> (row / p.K) & 1u)) continue;
+                const int k = sh ? p.dffs : p.dff;
+                const float4 q = __ldcg(reinterpret_cast<const float4*>(
+                    p.h32 + (sh ? h_shared : 0) + static_cast<size_t>(row) * k + col) + c.lane);
+                float v[4] = {q.x, q.y, q.z, q.w};
+                store_block<MODE>(v, sh ? hq_shared : p.hq, sh ? hs_shared : p.hs, row, k, col, c.lane);
             }
+            grid_barrier(c, 2);
+        }
+        ok = ok && *c.abort_flag == 0;
+        if (!epilogue) {
+            for_rows3(c, [&](int row0, int rows) {
+                load_tokens<MODE, 3>(c, Jobs3<MODE>(c, n_active, row0, rows), p.hq, p.hs, slots_h, p.dff, p.w2s, p.ws2s,
+                                     ring, ok);
+            });
+        } else {
+            float* out_s = reinterpret_cast<float*>(smem + OFF_OUT) + my_row;      // [t * 128]
+            for_rows3(c, [&](int row0, int rows) {
+                const bool in = my_row < rows;
+                for (int t = 0; t < p.T; ++t) out_s[t * 128] = 0.f;
+                for (Jobs3<MODE> jobs(c, n_active, row0, rows); jobs.next(j);) {
+                    // the block with an expert's first piece adds its bias
+                    const float bias = in && j.p0 == 0
+                        ? __ldg((j.shared ? p.bs2 : p.b2) + static_cast<size_t>(j.mat) * p.d + row0 + my_row) : 0.f;
+                    read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
+                        const float g = j.shared ? 1.f : gate_s[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)];
+                        out_s[t * 128] = fmaf(g, v + bias, out_s[t * 128]);
+                    });
+                }
+                if (p.split > 1) {
+                    // the last of the group's blocks adds the partial sums, in block order
+                    float* mine = p.sums + static_cast<size_t>(blockIdx.x) * p.T * 128 + my_row;
+                    for (int t = 0; t < p.T; ++t) __stcg(mine + t * 128, out_s[t * 128]);
+                    __threadfence();
+                    bar_epilogue();
+                    if (c.tid == 0) {
+                        uint32_t* ctr = p.ctr + CTR_GROUP + blockIdx.x / p.split;
+                        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(p.split - 1);
+                        if (last) *ctr = 0;
+                        __threadfence();
+                        misc[3] = last;
+                    }
+                    bar_epilogue();
+                    if (!misc[3]) return;
+                    const float* part = p.sums + static_cast<size_t>(blockIdx.x / p.split * p.split) * p.T * 128 + my_row;
+                    for (int t = 0; t < p.T; ++t) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int s = 0; s < MAX_SPLIT; ++s)
+                            if (s < p.split) v += __ldcg(part + (s * p.T + t) * 128);
+                        out_s[t * 128] = v;
+                    }
+                }
+                if (!in || !ok) return;
+                for (int t = 0; t < p.T; ++t) {
+                    float v = out_s[t * 128];
+                    const size_t at = static_cast<size_t>(t) * p.d + row0 + my_row;
+                    if (p.passthrough) {
+                        for (int k = 0; k < p.K; ++k)
+                            if (!(mask_s[idx_s[t * 16 + k]] >> t & 1u))
+                                v = fmaf(gate_s[t * 16 + k], __bfloat162float(p.x[at]), v);
+                    }
+                    p.out[at] = __float2bfloat16_rn(v);
+                }
+            });
         }
     }
+    tc_fence_before();
     __syncthreads();
     // the last block to leave zeroes the counters for the next launch
     if (c.tid == 0) {
@@ -944,25 +999,30 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
             __threadfence();
         }
     }
+    if (c.warp == W_MMA) {
+        tc_fence_after();
+        tmem_dealloc<TMEM_COLS>(tmem);
+    }
 }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 struct FewLayout {
-    size_t ctr, part, xq, xs, h32, hq, hs, total;
+    size_t ctr, part, xq, xs, h32, hq, hs, sums, total;
 };
 
 // blocks: as many as can find work, at most one per SM
 struct FewPlan {
-    int blocks, ks, slice;
+    int blocks, ks, slice, groups, split;
 };
 
 FewPlan few_plan(const Dims& dm, int sms) {
     FewPlan f;
     // a warp per (expert, slice); slices are multiples of 128 columns, at most
     // 5120 of them (16 tokens' slice of x fills the ring's memory)
-    static_assert(MAX_T * 5120 * 2 <= SLOTS * SLOT_BYTES, "the staged slice of x fits the ring");
-    const int want = (sms * CW + dm.E - 1) / dm.E;
+    static_assert(MAX_T * 5120 * 2 <= RING_BYTES, "the staged slice of x fits the ring");
+    int want = (sms * CW + dm.E - 1) / dm.E;
+    if (want > 16) want = 16;
     const int pieces = (dm.d + 127) / 128;
     int per = (pieces + want - 1) / want;
     if (per > 40) per = 40;
@@ -972,7 +1032,13 @@ FewPlan few_plan(const Dims& dm, int sms) {
     long long b = units;
     if (b < dm.d / 16) b = dm.d / 16;
     if (b < (f.ks * dm.E + CW - 1) / CW) b = (f.ks * dm.E + CW - 1) / CW;
+    if (sms > MAX_BLOCKS) sms = MAX_BLOCKS;
     f.blocks = b < sms ? static_cast<int>(b < 1 ? 1 : b) : sms;
+    // phase 3: as many blocks to a group of rows as bring its size near 128
+    const long long near = 128ll * f.blocks / dm.d;
+    f.split = near < 1 ? 1 : near > MAX_SPLIT ? MAX_SPLIT : static_cast<int>(near);
+    if (f.split > f.blocks) f.split = f.blocks;
+    f.groups = f.blocks / f.split;
     return f;
 }
 
@@ -980,25 +1046,34 @@ FewLayout few_layout(const Dims& dm) {
     FewLayout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off = align256(off + bytes); return o; };
-    const bool q = dm.dtype != MOE_BF16;
-    const size_t bb = dm.dtype == MOE_FP8_E4M3_BLOCK ? 1 : 2;
+    const bool q = dm.dtype != MOE_BF16, fp4 = dm.dtype == MOE_MXFP4;
     const size_t h = static_cast<size_t>(dm.T) * dm.K * dm.dff + static_cast<size_t>(dm.S) * dm.T * dm.dffs;
+    const size_t x = static_cast<size_t>(dm.T) * dm.d;
+    // bytes of n elements in operand form, and of their scales
+    auto form = [&](size_t n) { return fp4 ? n * PLANES / 2 : q ? n : 2 * n; };
+    auto scales = [&](size_t n) { return fp4 ? n * PLANES / 32 : q ? n / 128 * 4 : 0; };
     take(256);                                              // status word
-    L.ctr = take(256);
+    L.ctr = take((CTR_GROUP + MAX_BLOCKS) * 4);
     // slices are at least 128 columns long, whatever the device's size
     L.part = take(static_cast<size_t>((dm.d + 127) / 128) * dm.T * dm.E * 4);
-    L.xq = take(q ? static_cast<size_t>(dm.T) * dm.d * bb : 0);
-    L.xs = take(q ? static_cast<size_t>(dm.T) * (dm.d / 128) * 4 : 0);
+    L.xq = take(q ? form(x) : 0);
+    L.xs = take(scales(x));
     L.h32 = take(q ? h * 4 : 0);
-    L.hq = take(h * bb);
-    L.hs = take(q ? h / 128 * 4 : 0);
+    L.hq = take(form(h));
+    L.hs = take(scales(h));
+    L.sums = take(static_cast<size_t>(MAX_BLOCKS) * dm.T * 128 * 4);
     L.total = off;
     return L;
 }
 
-template <int MODE, int NT>
-cudaError_t launch_mode(const FewParams& p, int blocks, cudaStream_t st) {
-    auto kernel = few_tokens_kernel<MODE, NT>;
+template <int MODE>
+cudaError_t launch_mode(FewParams& p, int blocks, cudaStream_t st) {
+    // a slot: the piece, a row per column of the tokens, the scales
+    p.slot_bytes = PIECE_BYTES + ((round16(p.T * Form<MODE>::P) * 128 + 1023) & ~1023) + Form<MODE>::SF;
+    p.slots = RING_BYTES / p.slot_bytes < MAX_SLOTS ? RING_BYTES / p.slot_bytes : MAX_SLOTS;
+    static_assert(RING_BYTES / (PIECE_BYTES + round16(MAX_T * Form<MODE>::P) * 128 + Form<MODE>::SF) > LAG + 1,
+                  "the token side must not wait for slots that wait for it");
+    auto kernel = few_tokens_kernel<MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -1049,10 +1124,11 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     p.ctr = reinterpret_cast<uint32_t*>(w + L.ctr);
     p.part = reinterpret_cast<float*>(w + L.part);
     p.xq = dm.dtype == MOE_BF16 ? const_cast<uint8_t*>(static_cast<const uint8_t*>(a.x)) : w + L.xq;
-    p.xs = reinterpret_cast<float*>(w + L.xs);
+    p.xs = w + L.xs;
     p.h32 = reinterpret_cast<float*>(w + L.h32);
     p.hq = w + L.hq;
-    p.hs = reinterpret_cast<float*>(w + L.hs);
+    p.hs = w + L.hs;
+    p.sums = reinterpret_cast<float*>(w + L.sums);
     p.alpha = dm.alpha;
     p.T = dm.T;
     p.d = dm.d;
@@ -1066,7 +1142,9 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     p.passthrough = dm.passthrough;
     p.ks = plan.ks;
     p.slice = plan.slice;
-    const int most = (dm.d + plan.blocks - 1) / plan.blocks;
+    p.groups = plan.groups;
+    p.split = plan.split;
+    const int most = (dm.d + plan.groups - 1) / plan.groups;
     p.rows3 = most < 128 ? most : 128;
     const int elem = dm.dtype == MOE_BF16 ? 2 : 1;
     const int div = dm.dtype == MOE_MXFP4 ? 2 : 1;           // elements of K per map element
@@ -1076,12 +1154,9 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     if (dm.S > 0 && (!encode_tma_3d(&p.ws1, a.Ws1, dm.S, dm.dffs, dm.d / div, elem, 16) ||
                      !encode_tma_3d(&p.ws2, a.Ws2, dm.S, dm.d, dm.dffs / div, elem, p.rows3)))
         return cudaErrorInvalidValue;
-    const bool two = dm.T > 8;
-    if (dm.dtype == MOE_BF16)
-        return two ? launch_mode<M_BF16, 2>(p, plan.blocks, st) : launch_mode<M_BF16, 1>(p, plan.blocks, st);
-    if (dm.dtype == MOE_FP8_E4M3_BLOCK)
-        return two ? launch_mode<M_FP8, 2>(p, plan.blocks, st) : launch_mode<M_FP8, 1>(p, plan.blocks, st);
-    return two ? launch_mode<M_FP4, 2>(p, plan.blocks, st) : launch_mode<M_FP4, 1>(p, plan.blocks, st);
+    if (dm.dtype == MOE_BF16) return launch_mode<M_BF16>(p, plan.blocks, st);
+    if (dm.dtype == MOE_FP8_E4M3_BLOCK) return launch_mode<M_FP8>(p, plan.blocks, st);
+    return launch_mode<M_FP4>(p, plan.blocks, st);
 }
 
 }  // namespace moe

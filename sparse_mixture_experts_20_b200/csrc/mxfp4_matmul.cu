@@ -66,37 +66,6 @@ struct __align__(64) Mx4Params {
     uint8_t* y_scales;        // (rows, N/32), MXFP4 output
 };
 
-// Instruction descriptor of kind::mxf4.block_scale: E2M1 A and B (format 1,
-// bits 7-9 and 10-11), N >> 3 (17-22), UE8M0 scales (bit 23), M >> 7 (27-28),
-// and the byte offset (0 or 2) of the two scales of an MMA in its columns'
-// words (bits 4-5 for B, 29-30 for A).
-__host__ __device__ constexpr uint32_t make_idesc_mxf4(uint32_t sf_byte) {
-    return (sf_byte << 4) | (1u << 7) | (1u << 10) | ((BN >> 3) << 17) | (1u << 23) | ((BM >> 7) << 27) |
-           (sf_byte << 29);
-}
-
-__device__ __forceinline__ void umma_mxf4_bs(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
-        : "memory");
-}
-
-// 32 rows x 16 bytes (512 contiguous bytes of shared memory, groups of 8 rows
-// 128 bytes apart) to 4 columns of tensor memory, the same in every lane
-// quadrant.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, const void* src) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((smem_u32(src) & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(128u >> 4) << 16;
-    d |= static_cast<uint64_t>(128u >> 4) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(d) : "memory");
-}
-
 // The MMA thread's wait for a full stage: bounded, polling without the
 // suspend hint (this thread is on the critical path).
 static __device__ __noinline__ bool mma_wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -230,7 +199,7 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {          // 4 x 64 elements of K per stage
                         const uint32_t s = slot + 12 * (k >> 1);
-                        umma_mxf4_bs(d_tmem, adesc + 2 * k, bdesc + 2 * k, make_idesc_mxf4(2 * (k & 1)), s, s + 4,
+                        umma_mxf4_bs(d_tmem, adesc + 2 * k, bdesc + 2 * k, make_idesc_mxf4(BN, 2 * (k & 1)), s, s + 4,
                                      (kb > 0 || k > 0) ? 1u : 0u);
                     }
                     issued_any = true;
