@@ -2,25 +2,26 @@
 //
 // Decoding a few tokens is bound by the bytes of the experts they reach, so
 // the kernel is a stream of weight rows through every SM that nothing
-// interrupts: a warp loads pieces of up to 128 weight rows x 128 bytes by TMA
-// into a ring in shared memory, and tcgen05 multiplies them in place, the
-// weights as the 128-row operand and the tokens as a narrow one.  No thread
-// touches a weight; what the other warps do per piece is a few copies of the
-// token side.  One block per SM, launched cooperatively; the phases are
-// separated by grid barriers, and since weights do not depend on what the
-// barriers wait for, the ring keeps filling across them:
+// interrupts: a warp loads pieces of 128 weight rows x 128 bytes by TMA into a
+// ring in shared memory, and tcgen05 multiplies them in place, the weights as
+// the 128-row operand and the tokens as a narrow one.  No thread touches a
+// weight; what the other warps do per piece is a few copies of the token side.
+// One block per SM, launched cooperatively; the phases are separated by grid
+// barriers, and since weights do not depend on what the barriers wait for, the
+// ring keeps filling across them:
 //   1  router logits: (expert, slice of d) dot products in fp32, partial sums
 //      per slice; x into the operand form of the weights' type;
 //   -- barrier; every block then selects the top-K of all tokens for itself
-//      (slices added in order), builds the list of experts reached, and takes
-//      an equal share of their rows, 16 at a time:
+//      (slices added in order) and builds the list of experts reached;
 //   2  h = SiLU(W1 x + b1), written per (token, slot);
 //   -- barrier; FP8 and MXFP4: h into the operand form, barrier;
 //   3  out = sum over the experts of gate * (W2 h + b2), shared experts
-//      included.  The output rows are cut into groups of at most 128 and, to
-//      keep groups near that size (the tensor core reads 128 rows whatever the
-//      job has), the pieces of a group's experts are dealt to `split` blocks;
-//      the last of them to finish adds the partial sums in block order.
+//      included.
+// Phases 2 and 3 are one sequence each of tiles of 128 result rows (phase 2:
+// of every expert's W1; phase 3: of the output, through every expert's W2),
+// each a run of slots (two pieces of K).  Every block takes the same number of
+// slots; a tile that crosses a block boundary is summed from its blocks' parts,
+// in block order, by whichever of them finishes last.
 //
 // Operand forms (products exact, sums in fp32):
 //   bf16   weights, x and h in bf16 (kind::f16);
@@ -37,9 +38,8 @@
 //
 // Per block (320 threads):
 //   warps 0..3  epilogue (thread = row);   warps 4..7  token side: operand
-//   rows and all scales by cp.async, LAG pieces ahead;   (both: phase 1, the
-//   selection and the conversion of h)     warp 8  weights by TMA;
-//   warp 9  MMA issue.
+//   rows and all scales by cp.async;       (both: phase 1, the selection and
+//   the conversion of h)   warp 8  weights by TMA;   warp 9  MMA issue.
 // Every wait is bounded (common.cuh); after a wait gives up, the warps skip
 // the remaining work but keep meeting at the block's barriers.
 #include <cuda.h>
@@ -56,12 +56,12 @@ constexpr int CT = CW * 32;
 constexpr int W_TMA = 8, W_MMA = 9;
 constexpr int THREADS = CT + 64;
 constexpr int EPI = 128;                       // epilogue threads, and token-side threads
-constexpr int MAX_SLOTS = 11, PIECE_BYTES = 16384;
-constexpr int LAG = 4;                         // pieces of the token side in flight
+constexpr int NP = 2;                          // pieces per slot
+constexpr int MAX_SLOTS = 5, PIECE_BYTES = 16384;
 constexpr int MAX_T = MOE_FEW_MAX_TOKENS;
-constexpr int MAX_BLOCKS = 256, MAX_SPLIT = 8;
+constexpr int MAX_BLOCKS = 256;
 constexpr int PLANES = 5;                      // MXFP4: columns per token
-constexpr uint32_t ACC_COLS = 96, SF_COL0 = 2 * ACC_COLS, SF_SLOTS = 4, SF_COLS = 16, TMEM_COLS = 256;
+constexpr uint32_t ACC_COLS = 96, SF_COL0 = 2 * ACC_COLS, SF_COLS = 32, TMEM_COLS = 256;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -74,15 +74,15 @@ constexpr int OFF_OUT = OFF_ACT + 256 * 4;                     // [16][128] fp32
 constexpr int OFF_BAR = OFF_OUT + MAX_T * 128 * 4;             // full, empty [MAX_SLOTS]; accf, acce [2]; drain
 constexpr int OFF_MISC = OFF_BAR + (2 * MAX_SLOTS + 5) * 8;    // abort flag, n_active, tmem address, last flag, 8 warp counts
 constexpr int OFF_RING = (OFF_MISC + 64 + 1023) & ~1023;
-constexpr int RING_BYTES = 208 * 1024;
+constexpr int RING_BYTES = 207 * 1024;
 constexpr int SMEM_ALLOC = OFF_RING + RING_BYTES + 1024;
 static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
 static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
 static_assert(RING_BYTES >= MAX_T * 256 * 4 + 256 * 4, "the router's probabilities fit the ring's memory");
-static_assert(SF_COL0 + SF_SLOTS * SF_COLS <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
+static_assert(SF_COL0 + 2 * SF_COLS <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
 
 // grid-wide counters in the workspace, zero between launches
-enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_WORDS = 5, CTR_GROUP = 64 };
+enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_WORDS = 5, CTR_TILE = 64 };
 
 struct __align__(64) FewParams {
     CUtensorMap w1, w2, ws1, ws2;
@@ -105,19 +105,17 @@ struct __align__(64) FewParams {
     float* h32;                   // fp32 h: (T K, dff), then (S T, dffs)
     uint8_t* hq;                  // h in operand form, same rows (bf16: the only form)
     uint8_t* hs;                  // its scales
-    float* sums;                  // (blocks, T, 128) partial output sums
+    float* sums;                  // (blocks, 2, T, 128) parts of tiles that cross blocks
     float alpha;
     int T, d, E, K, dff, S, dffs, capacity, slot_major, passthrough;
     int ks, slice;                // router slices of d and their length
-    int groups, split;            // phase 3: row groups, blocks per group
-    int rows3;                    // rows of a phase-3 job (the W2 maps' box)
     int slots, slot_bytes;        // ring
 };
 
 enum { M_BF16 = 0, M_FP8 = 1, M_FP4 = 2 };
 
 // KP: elements of K in a piece (128 bytes of a weight row); P: columns per
-// token; SF: bytes of scales per slot (weights', then tokens')
+// token; SF: bytes of scales per piece (weights', then tokens')
 template <int MODE> struct Form;
 template <> struct Form<M_BF16> { static constexpr int KP = 64, P = 1, SF = 0; };
 template <> struct Form<M_FP8> { static constexpr int KP = 128, P = 1, SF = 1024; };
@@ -137,8 +135,11 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+// Arrives on bar once this thread's earlier cp.async copies have landed (the
+// barrier's count includes the arrival).
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     uint32_t v;
@@ -205,6 +206,11 @@ struct Ctx {
     int tid, warp, lane;
 };
 
+// Bounded wait on a phase of one of the block's barriers.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Ctx& c) {
+    return mbar_wait_bounded(bar, parity, c.abort_flag, c.p.status, kWaitNs);
+}
+
 // All consumer threads of all blocks.  Writes before it are visible to reads
 // (through L2) after it.
 __device__ void grid_barrier(const Ctx& c, int which) {
@@ -232,24 +238,20 @@ __device__ void grid_barrier(const Ctx& c, int which) {
 
 // ---------------------------------------------------------------- jobs
 
-// A job: `rows` (at most 128) consecutive rows of one matrix, streamed over
-// pieces p0 .. p1 - 1 of K (128 bytes of every row each), for the tokens of
+// A job: a run of slots of one tile and one matrix: pieces p0 .. p1 - 1 of K
+// (128 bytes of every row each) of rows row0 .. row0 + 127, for the tokens of
 // `mask`; the j-th of them has the columns j P .. j P + P - 1.
 struct Job {
     int shared;           // 1: shared expert
-    int mat, row0, rows;
+    int mat, row0;
     int n, k;             // the matrix: n rows of k columns
     int p0, p1;
     uint32_t mask;
     uint64_t kpack;       // routed: the tokens' slots
+    bool ends;            // the block's last job of this tile
+    // the blocks that have slots of this tile
+    int block0, block1;
 };
-
-__device__ __forceinline__ void set_matrix(const Ctx& c, Job& j, bool shared, int m) {
-    j.shared = shared;
-    j.mat = shared ? m : reinterpret_cast<const int*>(c.smem + OFF_ACT)[m];
-    j.mask = shared ? (1u << c.p.T) - 1u : reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK)[j.mat];
-    j.kpack = shared ? 0 : reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK)[j.mat];
-}
 
 // Row of the operand arrays of x (phase 2) or h (phase 3) for token t.
 template <int PHASE>
@@ -258,114 +260,111 @@ __device__ __forceinline__ int token_row(const Ctx& c, const Job& j, int t) {
     return j.shared ? j.mat * c.p.T + t : t * c.p.K + (static_cast<int>(j.kpack >> (4 * t)) & 15);
 }
 
-// Phase 2: this block's share of the rows of W1, in units of 16.
-template <int MODE>
-struct Jobs2 {
+// This block's share of a phase's slots, job by job.  Phase 2: matrix by
+// matrix, its tiles, their slots of K = d.  Phase 3: tile by tile, the shared
+// experts' slots, then those of the experts reached.
+template <int MODE, int PHASE>
+struct Jobs {
     const Ctx& c;
-    int u, end, n_shared;
-    __device__ __forceinline__ Jobs2(const Ctx& c_, int n_active) : c(c_) {
+    int at, end, all, parts;
+    int ss, sr;           // slots of a shared, a routed matrix per tile
+    int ts, tr;           // phase 2: tiles of a shared, a routed matrix
+    int tile;             // phase 3: slots of a tile
+    static __device__ __forceinline__ int slots_of(int k) { return (k + NP * Form<MODE>::KP - 1) / (NP * Form<MODE>::KP); }
+    __device__ __forceinline__ Jobs(const Ctx& c_, int n_active) : c(c_) {
         const FewParams& p = c.p;
-        n_shared = p.S * (p.dffs / 16);
-        const long long units = n_shared + static_cast<long long>(n_active) * (p.dff / 16);
-        u = static_cast<int>(units * blockIdx.x / gridDim.x);
-        end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+        if (PHASE == 2) {
+            ss = sr = slots_of(p.d);
+            ts = (p.dffs + 127) / 128;
+            tr = (p.dff + 127) / 128;
+            tile = 0;
+            all = (p.S * ts + n_active * tr) * sr;
+        } else {
+            ss = slots_of(p.dffs);
+            sr = slots_of(p.dff);
+            ts = tr = 1;
+            tile = p.S * ss + n_active * sr;
+            all = (p.d + 127) / 128 * tile;
+        }
+        // with fewer slots than blocks the last blocks have none, so that every
+        // block between a tile's first and last has some of it
+        parts = min(static_cast<int>(gridDim.x), all);
+        const int b = min(static_cast<int>(blockIdx.x), parts);
+        at = static_cast<int>(static_cast<long long>(all) * b / parts);
+        end = static_cast<int>(static_cast<long long>(all) * min(b + 1, parts) / parts);
     }
-    __device__ __forceinline__ bool next(Job& j) {
-        if (u >= end) return false;
-        const FewParams& p = c.p;
-        const bool sh = u < n_shared;
-        const int v = sh ? u : u - n_shared, per = sh ? p.dffs / 16 : p.dff / 16;
-        const int m = v / per, r = v % per;
-        const int run = min(end - u, per - r);
-        const int cuts = (run + 7) / 8, take = (run + cuts - 1) / cuts;
-        set_matrix(c, j, sh, m);
-        j.row0 = 16 * r;
-        j.rows = 16 * take;
-        j.n = sh ? p.dffs : p.dff;
-        j.k = p.d;
-        j.p0 = 0;
-        j.p1 = (p.d + Form<MODE>::KP - 1) / Form<MODE>::KP;
-        u += take;
-        return true;
-    }
-};
-
-// Phase 3: this block's share of the pieces that sum into rows row0 .. of the
-// output: the shared experts', then those of the experts reached.
-template <int MODE>
-struct Jobs3 {
-    const Ctx& c;
-    int row0, rows, at, end, ps, pr;
-    __device__ __forceinline__ Jobs3(const Ctx& c_, int n_active, int row0_, int rows_) : c(c_), row0(row0_), rows(rows_) {
-        const FewParams& p = c.p;
-        ps = (p.dffs + Form<MODE>::KP - 1) / Form<MODE>::KP;
-        pr = (p.dff + Form<MODE>::KP - 1) / Form<MODE>::KP;
-        const long long all = p.S * ps + static_cast<long long>(n_active) * pr;
-        const int s = blockIdx.x % p.split;
-        at = static_cast<int>(all * s / p.split);
-        end = static_cast<int>(all * (s + 1) / p.split);
+    // the block that has slot u
+    __device__ __forceinline__ int block_of(int u) const {
+        return static_cast<int>((static_cast<long long>(u + 1) * parts - 1) / all);
     }
     __device__ __forceinline__ bool next(Job& j) {
         if (at >= end) return false;
         const FewParams& p = c.p;
-        const bool sh = at < p.S * ps;
-        const int v = sh ? at : at - p.S * ps, per = sh ? ps : pr;
-        const int m = v / per, first = v % per;
-        set_matrix(c, j, sh, m);
-        j.row0 = row0;
-        j.rows = rows;
-        j.n = p.d;
-        j.k = sh ? p.dffs : p.dff;
-        j.p0 = first;
-        j.p1 = min(per, first + end - at);
-        at += j.p1 - j.p0;
+        int u = at, first = 0, m;
+        if (PHASE == 3) {
+            j.row0 = u / tile * 128;
+            first = u / tile * tile;
+            u -= first;
+        }
+        const int n_shared = p.S * ts * ss;
+        j.shared = u < n_shared;
+        if (!j.shared) u -= n_shared;
+        const int per = j.shared ? ss : sr, tiles = j.shared ? ts : tr;
+        const int run = u / per, s0 = u % per;                 // (matrix, tile), first slot of it
+        m = run / tiles;
+        if (PHASE == 2) {
+            j.row0 = run % tiles * 128;
+            first = at - s0;
+        }
+        const int take = min(per - s0, end - at);
+        j.mat = j.shared ? m : reinterpret_cast<const int*>(c.smem + OFF_ACT)[m];
+        j.mask = j.shared ? (1u << p.T) - 1u : reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK)[j.mat];
+        j.kpack = j.shared ? 0 : reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK)[j.mat];
+        const int inner = j.shared ? p.dffs : p.dff;
+        j.n = PHASE == 2 ? inner : p.d;
+        j.k = PHASE == 2 ? p.d : inner;
+        j.p0 = s0 * NP;
+        j.p1 = min((s0 + take) * NP, (j.k + Form<MODE>::KP - 1) / Form<MODE>::KP);
+        at += take;
+        const int last = first + (PHASE == 2 ? per : tile) - 1;
+        j.ends = at == end || at > last;
+        j.block0 = block_of(first);
+        j.block1 = block_of(last);
         return true;
     }
 };
 
-// The row ranges of phase 3 of this block, one after the other: body(row0, rows).
-template <typename F>
-__device__ __forceinline__ void for_rows3(const Ctx& c, F&& body) {
-    const FewParams& p = c.p;
-    const int g = blockIdx.x / p.split;
-    if (g >= p.groups) return;
-    const int begin = static_cast<int>(static_cast<long long>(p.d) * g / p.groups);
-    const int end = static_cast<int>(static_cast<long long>(p.d) * (g + 1) / p.groups);
-    for (int r = begin; r < end; r += p.rows3) body(r, min(p.rows3, end - r));
-}
-
-// A slot of the ring: the weights' piece, the tokens' rows, the scales.
 struct Ring {
     int slot = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next(int slots) { if (++slot == slots) { slot = 0; phase ^= 1u; } }
 };
 
+// A slot of the ring: NP pieces of weights, the tokens' rows of each, the
+// scales of each.
 __device__ __forceinline__ uint8_t* slot_at(const Ctx& c, int slot) { return c.smem + OFF_RING + slot * c.p.slot_bytes; }
-
 template <int MODE>
-__device__ __forceinline__ int scales_at(const Ctx& c) { return c.p.slot_bytes - Form<MODE>::SF; }
+__device__ __forceinline__ int rows_bytes(const Ctx& c) { return round16(c.p.T * Form<MODE>::P) * 128; }
+template <int MODE>
+__device__ __forceinline__ int scales_at(const Ctx& c) { return NP * (PIECE_BYTES + rows_bytes<MODE>(c)); }
 
 // ---------------------------------------------------------------- weights (one warp)
 
-// Loads a job's weights; false after a wait gave up.  box: rows of the tensor
-// map's box (16 in phase 2, rows3 in phase 3).
+// Loads a job's weights; false after a wait gave up.
 template <int MODE>
-__device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const CUtensorMap* map, int box, Ring& ring,
-                                             int& issued) {
-    const int boxes = (j.rows + box - 1) / box;
+__device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const CUtensorMap* map, Ring& ring) {
     constexpr int ELEMS = MODE == M_BF16 ? 64 : 128;        // map elements (bf16, or bytes) per piece
-    for (int s = j.p0; s < j.p1; ++s) {
+    for (int s = j.p0; s < j.p1; s += NP) {
         uint64_t* full = c.full + ring.slot;
+        const int np = min(NP, j.p1 - s);
         int ok = 1;
         if (c.lane == 0) {
-            ok = mbar_wait_bounded(c.empty + ring.slot, ring.phase ^ 1u, c.abort_flag, c.p.status, kWaitNs);
-            if (ok) mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * box * 128));
+            ok = wait(c.empty + ring.slot, ring.phase ^ 1u, c);
+            if (ok) mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * PIECE_BYTES));
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-        if (c.lane < boxes)
-            tma_load_3d(slot_at(c, ring.slot) + c.lane * box * 128, map, full, s * ELEMS, j.row0 + c.lane * box, j.mat);
-        ++issued;
+        if (c.lane < np)
+            tma_load_3d(slot_at(c, ring.slot) + c.lane * PIECE_BYTES, map, full, (s + c.lane) * ELEMS, j.row0, j.mat);
         ring.next(c.p.slots);
     }
     return true;
@@ -373,113 +372,112 @@ __device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const C
 
 // ---------------------------------------------------------------- token side (128 threads)
 
-// The tokens' operand rows and the scales of every piece of a phase's jobs, a
-// cp.async group per piece; a slot's arrival follows LAG pieces later, when
-// its group has landed.
-template <int MODE, int PHASE, typename Jobs>
-__device__ __forceinline__ void load_tokens(const Ctx& c, Jobs&& jobs, const uint8_t* base, const uint8_t* bscales,
-                                            int shared_row, int routed_k, const void* ws, const void* ws_shared,
-                                            Ring& ring, bool& ok) {
+// The tokens' operand rows and the scales of every piece of a phase's jobs,
+// copied by cp.async; the copies' own completion arrives on the slot's barrier.
+// (The tensor core reads them through the async proxy: the MMA thread, which
+// has nothing else in flight, makes the proxy fence.  Made here it would wait
+// for the copies just issued: measured 1000 cycles a piece.)
+template <int MODE, int PHASE>
+__device__ __forceinline__ void load_tokens(const Ctx& c, int n_active, const uint8_t* base, const uint8_t* bscales,
+                                            size_t shared_elems, const void* ws, const void* ws_shared, Ring& ring,
+                                            bool& ok) {
     constexpr int P = Form<MODE>::P, KP = Form<MODE>::KP;
-    constexpr int NB = P;                                      // operand rows a thread copies: 16 at a time, 16 P in all
     const int i = c.tid - EPI;
     const int q = i & 7;                                       // 16-byte chunk of a row's 128 bytes
     const int word = 16 * (i & 31) + 4 * (i >> 5);             // row i's word in 512 bytes of scales
-    Ring done = ring;
-    int pending = 0;
-    auto arrive = [&]() {
-        if (MODE == M_FP8) {
-            // the weight scale arrived as fp32: its UE8M0 byte, once per 32 columns
-            uint32_t* w = reinterpret_cast<uint32_t*>(slot_at(c, done.slot) + scales_at<MODE>(c) + word);
-            *w = ((*w >> 23) & 0xFFu) * 0x01010101u;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (c.lane == 0) mbar_arrive(c.full + done.slot);
-        done.next(c.p.slots);
-    };
+    const int row_bytes = rows_bytes<MODE>(c), sf_at = scales_at<MODE>(c);
+    Jobs<MODE, PHASE> jobs(c, n_active);
     Job j;
     while (ok && jobs.next(j)) {
         const int rows = __popc(j.mask) * P;
         // bytes of an operand row of j.k columns
         const size_t pitch = MODE == M_BF16 ? 2 * static_cast<size_t>(j.k) : MODE == M_FP8 ? j.k : j.k / 2;
+        const int kq = MODE == M_FP8 ? j.k / 128 * 4 : j.k / 32;   // and of its scales
         // shared experts' rows of h follow the routed ones, at their own width
         const uint8_t* data = base;
         const uint8_t* sc = bscales;
         if (PHASE == 3 && j.shared) {
-            const size_t skip = static_cast<size_t>(shared_row) * P * routed_k;     // elements
+            const size_t skip = shared_elems * P;
             data += MODE == M_BF16 ? 2 * skip : MODE == M_FP8 ? skip : skip / 2;
             sc += MODE == M_FP8 ? skip / 128 * 4 : skip / 32;
         }
         auto operand_row = [&](int n) {                        // of column n
             uint32_t m = j.mask;
             for (int z = n / P; z > 0; --z) m &= m - 1;
-            return token_row<PHASE>(c, j, __ffs(m) - 1) * P + n % P;
+            return static_cast<size_t>(token_row<PHASE>(c, j, __ffs(m) - 1) * P + n % P);
         };
-        const uint8_t* src[NB];
+        const uint8_t* src[P];                                 // 16 rows at a time, 16 P in all
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < P; ++b) {
             const int n = (i >> 3) + 16 * b;
             src[b] = n < rows ? data + operand_row(n) * pitch + 16 * q : nullptr;
         }
         const uint8_t* bs = nullptr;                           // scales of column i
         const uint8_t* as = nullptr;                           // scales of weight row i
-        const int kq = MODE == M_FP8 ? j.k / 128 * 4 : j.k / 32;
         if (MODE != M_BF16) {
-            if (i < rows) bs = sc + static_cast<size_t>(operand_row(i)) * kq;
-            if (i < j.rows && j.row0 + i < j.n) {
+            if (i < rows) bs = sc + operand_row(i) * kq;
+            if (j.row0 + i < j.n) {
                 const uint8_t* w = static_cast<const uint8_t*>(j.shared ? ws_shared : ws);
-                as = MODE == M_FP8 ? w + (static_cast<size_t>(j.mat) * (j.n / 128) + (j.row0 + i) / 128) * kq
+                as = MODE == M_FP8 ? w + (static_cast<size_t>(j.mat) * (j.n / 128) + j.row0 / 128) * kq
                                    : w + (static_cast<size_t>(j.mat) * j.n + j.row0 + i) * kq;
             }
         }
-        for (int s = j.p0; s < j.p1; ++s) {
+        float wsc[NP];                                         // FP8: the tile's weight scales, a slot ahead
+        auto fetch = [&](int s) {
+#pragma unroll
+            for (int r = 0; r < NP; ++r)
+                wsc[r] = s + r < j.p1 ? __ldg(reinterpret_cast<const float*>(as) + s + r) : 0.f;
+        };
+        if (MODE == M_FP8) fetch(j.p0);
+        for (int s = j.p0; s < j.p1; s += NP) {
             int w = 1;
-            if (c.lane == 0) w = mbar_wait_bounded(c.empty + ring.slot, ring.phase ^ 1u, c.abort_flag, c.p.status, kWaitNs);
+            if (c.lane == 0) w = wait(c.empty + ring.slot, ring.phase ^ 1u, c);
             if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
             uint8_t* slot = slot_at(c, ring.slot);
-            uint8_t* bdst = slot + PIECE_BYTES;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int n = (i >> 3) + 16 * b;
-                if (src[b] && (MODE != M_FP4 || static_cast<size_t>(s) * 128 + 16 * q < pitch))
-                    cp_async_16(bdst + n * 128 + ((q ^ (n & 7)) << 4), src[b] + static_cast<size_t>(s) * 128);
-            }
-            if (MODE != M_BF16) {
-                uint8_t* sf = slot + scales_at<MODE>(c) + word;
+            for (int r = 0; r < NP; ++r) {
+                const int piece = s + r;
+                if (piece >= j.p1) break;
+                uint8_t* bdst = slot + NP * PIECE_BYTES + r * row_bytes;
+#pragma unroll
+                for (int b = 0; b < P; ++b) {
+                    const int n = (i >> 3) + 16 * b;
+                    if (src[b] && (MODE != M_FP4 || static_cast<size_t>(piece) * 128 + 16 * q < pitch))
+                        cp_async_16(bdst + n * 128 + ((q ^ (n & 7)) << 4), src[b] + static_cast<size_t>(piece) * 128);
+                }
+                uint8_t* sf = slot + sf_at + r * Form<MODE>::SF + word;
                 if (MODE == M_FP8) {
-                    if (as) cp_async_4(sf, as + 4 * s);
-                    if (bs) cp_async_4(sf + 512, bs + 4 * s);
-                } else {
-                    const bool two = s * KP + 128 < j.k;       // the piece's second 128 columns exist
+                    // the weight scale's UE8M0 byte, once per 32 columns
+                    *reinterpret_cast<uint32_t*>(sf) = ((__float_as_uint(wsc[r]) >> 23) & 0xFFu) * 0x01010101u;
+                    if (bs) cp_async_4(sf + 512, bs + 4 * piece);
+                }
+                if (MODE == M_FP4) {
+                    const bool two = piece * KP + 128 < j.k;   // the piece's second 128 columns exist
                     if (as) {
-                        cp_async_4(sf, as + 8 * s);
-                        if (two) cp_async_4(sf + 512, as + 8 * s + 4);
+                        cp_async_4(sf, as + 8 * piece);
+                        if (two) cp_async_4(sf + 512, as + 8 * piece + 4);
                     }
                     if (bs) {
-                        cp_async_4(sf + 1024, bs + 8 * s);
-                        if (two) cp_async_4(sf + 1536, bs + 8 * s + 4);
+                        cp_async_4(sf + 1024, bs + 8 * piece);
+                        if (two) cp_async_4(sf + 1536, bs + 8 * piece + 4);
                     }
                 }
             }
-            cp_async_commit();
-            ring.next(c.p.slots);
-            if (++pending > LAG) {
-                cp_async_wait<LAG>();
-                arrive();
-                --pending;
+            cp_async_arrive(c.full + ring.slot);
+            if (MODE == M_FP8) {
+                mbar_arrive(c.full + ring.slot);               // the scales stored above
+                fetch(s + NP);
             }
+            ring.next(c.p.slots);
         }
     }
-    cp_async_wait<0>();
-    for (; pending > 0; --pending) arrive();
 }
 
 // ---------------------------------------------------------------- MMA issue (one thread)
 
 struct MmaState {
     Ring ring;
-    int jobs = 0, pieces = 0;
+    int jobs = 0, slots = 0;
     bool issued = false;
 };
 
@@ -487,41 +485,42 @@ template <int MODE>
 __device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, uint32_t tmem, uint64_t* accf, uint64_t* acce,
                                           MmaState& st) {
     const int buf = st.jobs & 1;
-    if (!mbar_wait_bounded(acce + buf, ((st.jobs >> 1) & 1) ^ 1u, c.abort_flag, c.p.status, kWaitNs)) return false;
+    if (!wait(acce + buf, ((st.jobs >> 1) & 1) ^ 1u, c)) return false;
     tc_fence_after();
     const uint32_t d = tmem + buf * ACC_COLS;
     const uint32_t n = round16(__popc(j.mask) * Form<MODE>::P);
-    uint32_t idesc;
-    if (MODE == M_BF16) idesc = make_idesc(1, 128, n);
-    else if (MODE == M_FP8) idesc = make_idesc_mxf8(128, n);
-    else idesc = 0;                                            // made per MMA below
-    for (int s = j.p0; s < j.p1; ++s) {
-        if (!mbar_wait_bounded(c.full + st.ring.slot, st.ring.phase, c.abort_flag, c.p.status, kWaitNs)) return false;
+    const int row_bytes = rows_bytes<MODE>(c), sf_at = scales_at<MODE>(c);
+    for (int s = j.p0; s < j.p1; s += NP) {
+        if (!wait(c.full + st.ring.slot, st.ring.phase, c)) return false;
+        fence_proxy_async_smem();                              // the token side was copied through the generic proxy
         uint8_t* slot = slot_at(c, st.ring.slot);
-        const uint64_t a = smem_desc_k_sw128(slot), b = smem_desc_k_sw128(slot + PIECE_BYTES);
-        const uint32_t more = s > j.p0 ? 1u : 0u;
-        if (MODE == M_BF16) {
-            tc_fence_after();
+        if (MODE != M_BF16 && st.slots >= 2) {
+            // the MMAs that read this half of the scale columns two slots ago are done
+            int q = st.ring.slot - 2;
+            uint32_t ph = st.ring.phase;
+            if (q < 0) { q += c.p.slots; ph ^= 1u; }
+            if (!wait(c.empty + q, ph, c)) return false;
+        }
+        tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, idesc, more | (k > 0));
-        } else {
-            // the MMAs that read this slot of scales SF_SLOTS pieces ago are done
-            if (st.pieces >= static_cast<int>(SF_SLOTS)) {
-                int q = st.ring.slot - static_cast<int>(SF_SLOTS);
-                uint32_t ph = st.ring.phase;
-                if (q < 0) { q += c.p.slots; ph ^= 1u; }
-                if (!mbar_wait_bounded(c.empty + q, ph, c.abort_flag, c.p.status, kWaitNs)) return false;
-            }
-            tc_fence_after();
-            const uint8_t* sf = slot + scales_at<MODE>(c);
-            const uint32_t t = tmem + SF_COL0 + (st.pieces % SF_SLOTS) * SF_COLS;
-            if (MODE == M_FP8) {
+        for (int r = 0; r < NP; ++r) {
+            if (s + r >= j.p1) break;
+            const uint64_t a = smem_desc_k_sw128(slot + r * PIECE_BYTES);
+            const uint64_t b = smem_desc_k_sw128(slot + NP * PIECE_BYTES + r * row_bytes);
+            const uint32_t more = s + r > j.p0 ? 1u : 0u;
+            const uint8_t* sf = slot + sf_at + r * Form<MODE>::SF;
+            const uint32_t t = tmem + SF_COL0 + (st.slots & 1) * SF_COLS + r * (SF_COLS / NP);
+            if (MODE == M_BF16) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, make_idesc(1, 128, n), more | (k > 0));
+            } else if (MODE == M_FP8) {
                 tmem_cp_scales(t, sf);
                 tmem_cp_scales(t + 4, sf + 512);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_mxf8_bs(d, a + 2 * k, b + 2 * k, idesc, t, t + 4, more | (k > 0));
+                for (int k = 0; k < 4; ++k)
+                    umma_mxf8_bs(d, a + 2 * k, b + 2 * k, make_idesc_mxf8(128, n), t, t + 4, more | (k > 0));
             } else {
-                const bool two = s * Form<MODE>::KP + 128 < j.k;
+                const bool two = (s + r) * Form<MODE>::KP + 128 < j.k;
                 tmem_cp_scales(t, sf);
                 tmem_cp_scales(t + 8, sf + 1024);
                 if (two) {
@@ -532,11 +531,11 @@ __device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, uint32_t t
                 for (int k = 0; k < 4; ++k)
                     if (k < 2 || two)
                         umma_mxf4_bs(d, a + 2 * k, b + 2 * k, make_idesc_mxf4(n, 2 * (k & 1)), t + 4 * (k >> 1),
-                                  t + 8 + 4 * (k >> 1), more | (k > 0));
+                                     t + 8 + 4 * (k >> 1), more | (k > 0));
             }
         }
         st.issued = true;
-        ++st.pieces;
+        ++st.slots;
         umma_commit(c.empty + st.ring.slot);
         st.ring.next(c.p.slots);
     }
@@ -555,7 +554,7 @@ __device__ __forceinline__ void read_job(const Ctx& c, const Job& j, uint32_t tm
     const int buf = jobs & 1;
     if (ok) {
         int w = 1;
-        if (c.lane == 0) w = mbar_wait_bounded(accf + buf, (jobs >> 1) & 1, c.abort_flag, c.p.status, kWaitNs);
+        if (c.lane == 0) w = wait(accf + buf, (jobs >> 1) & 1, c);
         ok = __shfl_sync(0xffffffffu, w, 0) != 0;
     }
     ++jobs;
@@ -591,6 +590,45 @@ __device__ __forceinline__ void read_job(const Ctx& c, const Job& j, uint32_t tm
     }
 }
 
+// A tile that crosses blocks: stores this block's sums (sums[t * 128] for the
+// thread's row, tokens of `mask`), and in the last of the tile's blocks to get
+// here replaces them by the total over the blocks, in block order.  True where
+// the sums are now the tile's.  Every epilogue thread calls it.
+__device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mask, float* sums) {
+    const FewParams& p = c.p;
+    if (j.block0 == j.block1) return true;
+    const int b = blockIdx.x;
+    // a block has at most one tile it continues and one it leaves unfinished
+    auto part = [&](int blk) { return p.sums + (static_cast<size_t>(blk) * 2 + (blk == j.block0)) * p.T * 128 + c.tid; };
+    float* mine = part(b);
+    for (uint32_t m = mask; m; m &= m - 1) {
+        const int t = __ffs(m) - 1;
+        __stcg(mine + t * 128, sums[t * 128]);
+    }
+    int* last_s = reinterpret_cast<int*>(c.smem + OFF_MISC) + 3;
+    __threadfence();
+    bar_epilogue();
+    if (c.tid == 0) {
+        uint32_t* ctr = p.ctr + CTR_TILE + j.block0;
+        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(j.block1 - j.block0);
+        if (last) *ctr = 0;
+        __threadfence();
+        *last_s = last;
+    }
+    bar_epilogue();
+    const bool last = *last_s != 0;
+    bar_epilogue();                                            // the flag may be written again
+    if (!last) return false;
+    for (uint32_t m = mask; m; m &= m - 1) {
+        const int t = __ffs(m) - 1;
+        float v = 0.f;
+#pragma unroll 4
+        for (int blk = j.block0; blk <= j.block1; ++blk) v += __ldcg(part(blk) + t * 128);
+        sums[t * 128] = v;
+    }
+    return true;
+}
+
 // ---------------------------------------------------------------- phase 1
 
 template <int MODE>
@@ -606,16 +644,13 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
             store_block<MODE>(v, p.xq, p.xs, t, p.d, b * 128, c.lane);
         }
     }
-    // items (slice, expert), slice-major: a block mostly stays in one slice of
-    // x, which it stages in the ring's memory
-    const int items = p.ks * p.E;
-    int i0 = static_cast<int>(static_cast<long long>(items) * blockIdx.x / gridDim.x);
-    const int i1 = static_cast<int>(static_cast<long long>(items) * (blockIdx.x + 1) / gridDim.x);
+    // a block has one slice of d and a share of the experts; it stages the
+    // tokens' slices in the ring's memory
+    const int sharers = gridDim.x / p.ks, who = blockIdx.x / p.ks, ks = blockIdx.x % p.ks;
     __nv_bfloat16* xsm = reinterpret_cast<__nv_bfloat16*>(c.smem + OFF_RING);
-    while (i0 < i1) {
-        const int ks = i0 / p.E, e0 = i0 % p.E, e1 = min(p.E, e0 + i1 - i0);
+    if (who < sharers) {
+        const int e0 = p.E * who / sharers, e1 = p.E * (who + 1) / sharers;
         const int k0 = ks * p.slice, len = min(p.slice, p.d - k0);       // multiples of 64
-        bar_consumers();
         for (int i = c.tid; i < p.T * (len / 8); i += CT) {
             const int t = i / (len / 8), q = i % (len / 8);
             reinterpret_cast<uint4*>(xsm + t * p.slice)[q] =
@@ -648,7 +683,6 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
                 if (c.lane == t) p.part[(static_cast<size_t>(ks) * p.T + t) * p.E + e] = v;
             }
         }
-        i0 += e1 - e0;
     }
 }
 
@@ -818,7 +852,8 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
                 static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31)};
     if (c.tid == 0) {
         for (int i = 0; i < p.slots; ++i) {
-            mbar_init(c.full + i, 1 + 4);                       // expect_tx, the four token-side warps
+            // expect_tx; the token side's copies and, in FP8, stores
+            mbar_init(c.full + i, 1 + EPI * (MODE == M_FP8 ? 2 : 1));
             mbar_init(c.empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) { mbar_init(accf + i, 1); mbar_init(acce + i, EPI); }
@@ -841,18 +876,15 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         __syncthreads();                                        // the experts are selected
         const int n_active = misc[1];
         Ring ring;
-        int issued = 0;
         bool ok = *c.abort_flag == 0;
         Job j;
-        for (Jobs2<MODE> jobs(c, n_active); ok && jobs.next(j);)
-            ok = load_weights<MODE>(c, j, j.shared ? &p.ws1 : &p.w1, 16, ring, issued);
-        for_rows3(c, [&](int row0, int rows) {
-            for (Jobs3<MODE> jobs(c, n_active, row0, rows); ok && jobs.next(j);)
-                ok = load_weights<MODE>(c, j, j.shared ? &p.ws2 : &p.w2, p.rows3, ring, issued);
-        });
-        // copies in flight land before the block gives its memory back (only
-        // the weights' bytes are waited for where the token side gave up: its
-        // arrivals are made good here)
+        for (Jobs<MODE, 2> jobs(c, n_active); ok && jobs.next(j);)
+            ok = load_weights<MODE>(c, j, j.shared ? &p.ws1 : &p.w1, ring);
+        for (Jobs<MODE, 3> jobs(c, n_active); ok && jobs.next(j);)
+            ok = load_weights<MODE>(c, j, j.shared ? &p.ws2 : &p.w2, ring);
+        // a block that gave up leaves its copies the time to land before it
+        // gives its memory back (their barriers may never complete, since the
+        // token side stopped arriving)
         if (!ok && c.lane == 0) {
             const uint64_t t0 = global_timer_ns();
             while (global_timer_ns() - t0 < kDrainNs) {}
@@ -865,11 +897,8 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
             MmaState st;
             bool ok = *c.abort_flag == 0;
             Job j;
-            for (Jobs2<MODE> jobs(c, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
-            for_rows3(c, [&](int row0, int rows) {
-                for (Jobs3<MODE> jobs(c, n_active, row0, rows); ok && jobs.next(j);)
-                    ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
-            });
+            for (Jobs<MODE, 2> jobs(c, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
+            for (Jobs<MODE, 3> jobs(c, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
             if (!ok && st.issued) {
                 umma_commit(drain);
                 volatile int no_abort = 0;
@@ -886,27 +915,30 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         const int slots_h = p.T * p.K;                          // rows of routed h
         const size_t h_shared = static_cast<size_t>(slots_h) * p.dff;
         const bool epilogue = c.warp < 4;
-        const int my_row = c.tid;                               // epilogue: this thread's row of a job
+        const int my_row = c.tid;                               // epilogue: this thread's row of a tile
+        float* sums = reinterpret_cast<float*>(smem + OFF_OUT) + my_row;           // [t * 128]
         Ring ring;
         int jobs_read = 0;
         bool ok = *c.abort_flag == 0;
         Job j;
         if (epilogue) {
-            for (Jobs2<MODE> jobs(c, n_active); jobs.next(j);) {
-                const bool in = my_row < j.rows;
+            for (Jobs<MODE, 2> jobs(c, n_active); jobs.next(j);) {
+                const bool in = j.row0 + my_row < j.n;
                 const float bias = in ? __ldg((j.shared ? p.bs1 : p.b1) + static_cast<size_t>(j.mat) * j.n + j.row0 + my_row)
                                       : 0.f;
+                read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) { sums[t * 128] = v; });
+                if (!combine(c, j, j.mask, sums) || !in) continue;
                 const size_t base = j.shared ? h_shared : 0;
-                read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
-                    if (!in) return;
-                    const float h = silu_fast(v + bias);
+                for (uint32_t m = j.mask; m; m &= m - 1) {
+                    const int t = __ffs(m) - 1;
+                    const float h = silu_fast(sums[t * 128] + bias);
                     const size_t at = base + static_cast<size_t>(token_row<3>(c, j, t)) * j.n + j.row0 + my_row;
                     if (MODE == M_BF16) reinterpret_cast<__nv_bfloat16*>(p.hq)[at] = __float2bfloat16_rn(h);
                     else p.h32[at] = h;
-                });
+                }
             }
         } else {
-            load_tokens<MODE, 2>(c, Jobs2<MODE>(c, n_active), p.xq, p.xs, 0, 0, p.w1s, p.ws1s, ring, ok);
+            load_tokens<MODE, 2>(c, n_active, p.xq, p.xs, 0, p.w1s, p.ws1s, ring, ok);
         }
         grid_barrier(c, 1);
         const int* idx_s = reinterpret_cast<const int*>(smem + OFF_IDX);
@@ -933,52 +965,26 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         }
         ok = ok && *c.abort_flag == 0;
         if (!epilogue) {
-            for_rows3(c, [&](int row0, int rows) {
-                load_tokens<MODE, 3>(c, Jobs3<MODE>(c, n_active, row0, rows), p.hq, p.hs, slots_h, p.dff, p.w2s, p.ws2s,
-                                     ring, ok);
-            });
+            load_tokens<MODE, 3>(c, n_active, p.hq, p.hs, h_shared, p.w2s, p.ws2s, ring, ok);
         } else {
-            float* out_s = reinterpret_cast<float*>(smem + OFF_OUT) + my_row;      // [t * 128]
-            for_rows3(c, [&](int row0, int rows) {
-                const bool in = my_row < rows;
-                for (int t = 0; t < p.T; ++t) out_s[t * 128] = 0.f;
-                for (Jobs3<MODE> jobs(c, n_active, row0, rows); jobs.next(j);) {
-                    // the block with an expert's first piece adds its bias
-                    const float bias = in && j.p0 == 0
-                        ? __ldg((j.shared ? p.bs2 : p.b2) + static_cast<size_t>(j.mat) * p.d + row0 + my_row) : 0.f;
-                    read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
-                        const float g = j.shared ? 1.f : gate_s[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)];
-                        out_s[t * 128] = fmaf(g, v + bias, out_s[t * 128]);
-                    });
-                }
-                if (p.split > 1) {
-                    // the last of the group's blocks adds the partial sums, in block order
-                    float* mine = p.sums + static_cast<size_t>(blockIdx.x) * p.T * 128 + my_row;
-                    for (int t = 0; t < p.T; ++t) __stcg(mine + t * 128, out_s[t * 128]);
-                    __threadfence();
-                    bar_epilogue();
-                    if (c.tid == 0) {
-                        uint32_t* ctr = p.ctr + CTR_GROUP + blockIdx.x / p.split;
-                        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(p.split - 1);
-                        if (last) *ctr = 0;
-                        __threadfence();
-                        misc[3] = last;
-                    }
-                    bar_epilogue();
-                    if (!misc[3]) return;
-                    const float* part = p.sums + static_cast<size_t>(blockIdx.x / p.split * p.split) * p.T * 128 + my_row;
-                    for (int t = 0; t < p.T; ++t) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int s = 0; s < MAX_SPLIT; ++s)
-                            if (s < p.split) v += __ldcg(part + (s * p.T + t) * 128);
-                        out_s[t * 128] = v;
-                    }
-                }
-                if (!in || !ok) return;
+            const uint32_t every = (1u << p.T) - 1u;
+            bool begins = true;
+            for (Jobs<MODE, 3> jobs(c, n_active); jobs.next(j);) {
+                if (begins) for (int t = 0; t < p.T; ++t) sums[t * 128] = 0.f;
+                begins = j.ends;
+                const int row = j.row0 + my_row;
+                const bool in = row < p.d;
+                // the block with a matrix's first piece adds its bias
+                const float bias = in && j.p0 == 0
+                    ? __ldg((j.shared ? p.bs2 : p.b2) + static_cast<size_t>(j.mat) * p.d + row) : 0.f;
+                read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
+                    const float g = j.shared ? 1.f : gate_s[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)];
+                    sums[t * 128] = fmaf(g, v + bias, sums[t * 128]);
+                });
+                if (!j.ends || !combine(c, j, every, sums) || !in || !ok) continue;
                 for (int t = 0; t < p.T; ++t) {
-                    float v = out_s[t * 128];
-                    const size_t at = static_cast<size_t>(t) * p.d + row0 + my_row;
+                    float v = sums[t * 128];
+                    const size_t at = static_cast<size_t>(t) * p.d + row;
                     if (p.passthrough) {
                         for (int k = 0; k < p.K; ++k)
                             if (!(mask_s[idx_s[t * 16 + k]] >> t & 1u))
@@ -986,7 +992,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
                     }
                     p.out[at] = __float2bfloat16_rn(v);
                 }
-            });
+            }
         }
     }
     tc_fence_before();
@@ -1013,32 +1019,34 @@ struct FewLayout {
 
 // blocks: as many as can find work, at most one per SM
 struct FewPlan {
-    int blocks, ks, slice, groups, split;
+    int blocks, ks, slice;
 };
 
 FewPlan few_plan(const Dims& dm, int sms) {
     FewPlan f;
-    // a warp per (expert, slice); slices are multiples of 128 columns, at most
-    // 5120 of them (16 tokens' slice of x fills the ring's memory)
+    if (sms > MAX_BLOCKS) sms = MAX_BLOCKS;
+    // a block per slot of weights that the most experts reached would have
+    const int kp = dm.dtype == MOE_BF16 ? Form<M_BF16>::KP : dm.dtype == MOE_MXFP4 ? Form<M_FP4>::KP : Form<M_FP8>::KP;
+    auto slots = [&](long long rows, long long k) { return (rows + 127) / 128 * ((k + NP * kp - 1) / (NP * kp)); };
+    const long long reached = dm.T * dm.K < dm.E ? dm.T * dm.K : dm.E;
+    const long long s2 = reached * slots(dm.dff, dm.d) + dm.S * slots(dm.dffs, dm.d);
+    const long long s3 = reached * slots(dm.d, dm.dff) + dm.S * slots(dm.d, dm.dffs);
+    const long long most = s2 > s3 ? s2 : s3;
+    f.blocks = most < sms ? static_cast<int>(most) : sms;
+    // router: slices of d (multiples of 128 columns, at most 5120: 16 tokens'
+    // slice fills the ring's memory), as many as give each block at most one
+    // expert a warp
     static_assert(MAX_T * 5120 * 2 <= RING_BYTES, "the staged slice of x fits the ring");
-    int want = (sms * CW + dm.E - 1) / dm.E;
+    int want = f.blocks * CW / dm.E;
     if (want > 16) want = 16;
+    if (want > f.blocks) want = f.blocks;
+    if (want < 1) want = 1;
     const int pieces = (dm.d + 127) / 128;
     int per = (pieces + want - 1) / want;
     if (per > 40) per = 40;
     f.slice = 128 * per;
     f.ks = (pieces + per - 1) / per;
-    const long long units = (static_cast<long long>(dm.T) * dm.K * dm.dff + static_cast<long long>(dm.S) * dm.dffs) / 16;
-    long long b = units;
-    if (b < dm.d / 16) b = dm.d / 16;
-    if (b < (f.ks * dm.E + CW - 1) / CW) b = (f.ks * dm.E + CW - 1) / CW;
-    if (sms > MAX_BLOCKS) sms = MAX_BLOCKS;
-    f.blocks = b < sms ? static_cast<int>(b < 1 ? 1 : b) : sms;
-    // phase 3: as many blocks to a group of rows as bring its size near 128
-    const long long near = 128ll * f.blocks / dm.d;
-    f.split = near < 1 ? 1 : near > MAX_SPLIT ? MAX_SPLIT : static_cast<int>(near);
-    if (f.split > f.blocks) f.split = f.blocks;
-    f.groups = f.blocks / f.split;
+    if (f.blocks < f.ks) f.blocks = f.ks;
     return f;
 }
 
@@ -1053,7 +1061,7 @@ FewLayout few_layout(const Dims& dm) {
     auto form = [&](size_t n) { return fp4 ? n * PLANES / 2 : q ? n : 2 * n; };
     auto scales = [&](size_t n) { return fp4 ? n * PLANES / 32 : q ? n / 128 * 4 : 0; };
     take(256);                                              // status word
-    L.ctr = take((CTR_GROUP + MAX_BLOCKS) * 4);
+    L.ctr = take((CTR_TILE + MAX_BLOCKS) * 4);
     // slices are at least 128 columns long, whatever the device's size
     L.part = take(static_cast<size_t>((dm.d + 127) / 128) * dm.T * dm.E * 4);
     L.xq = take(q ? form(x) : 0);
@@ -1061,18 +1069,17 @@ FewLayout few_layout(const Dims& dm) {
     L.h32 = take(q ? h * 4 : 0);
     L.hq = take(form(h));
     L.hs = take(scales(h));
-    L.sums = take(static_cast<size_t>(MAX_BLOCKS) * dm.T * 128 * 4);
+    L.sums = take(static_cast<size_t>(MAX_BLOCKS) * 2 * dm.T * 128 * 4);
     L.total = off;
     return L;
 }
 
 template <int MODE>
 cudaError_t launch_mode(FewParams& p, int blocks, cudaStream_t st) {
-    // a slot: the piece, a row per column of the tokens, the scales
-    p.slot_bytes = PIECE_BYTES + ((round16(p.T * Form<MODE>::P) * 128 + 1023) & ~1023) + Form<MODE>::SF;
+    constexpr int rows_max = round16(MAX_T * Form<MODE>::P) * 128;
+    static_assert(RING_BYTES / (NP * (PIECE_BYTES + rows_max + Form<MODE>::SF)) >= 3, "two slots of MMAs in flight");
+    p.slot_bytes = NP * (PIECE_BYTES + round16(p.T * Form<MODE>::P) * 128 + Form<MODE>::SF);
     p.slots = RING_BYTES / p.slot_bytes < MAX_SLOTS ? RING_BYTES / p.slot_bytes : MAX_SLOTS;
-    static_assert(RING_BYTES / (PIECE_BYTES + round16(MAX_T * Form<MODE>::P) * 128 + Form<MODE>::SF) > LAG + 1,
-                  "the token side must not wait for slots that wait for it");
     auto kernel = few_tokens_kernel<MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
     if (e != cudaSuccess) return e;
@@ -1142,17 +1149,13 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     p.passthrough = dm.passthrough;
     p.ks = plan.ks;
     p.slice = plan.slice;
-    p.groups = plan.groups;
-    p.split = plan.split;
-    const int most = (dm.d + plan.groups - 1) / plan.groups;
-    p.rows3 = most < 128 ? most : 128;
     const int elem = dm.dtype == MOE_BF16 ? 2 : 1;
     const int div = dm.dtype == MOE_MXFP4 ? 2 : 1;           // elements of K per map element
-    if (!encode_tma_3d(&p.w1, a.W1, dm.E, dm.dff, dm.d / div, elem, 16) ||
-        !encode_tma_3d(&p.w2, a.W2, dm.E, dm.d, dm.dff / div, elem, p.rows3))
+    if (!encode_tma_3d(&p.w1, a.W1, dm.E, dm.dff, dm.d / div, elem, 128) ||
+        !encode_tma_3d(&p.w2, a.W2, dm.E, dm.d, dm.dff / div, elem, 128))
         return cudaErrorInvalidValue;
-    if (dm.S > 0 && (!encode_tma_3d(&p.ws1, a.Ws1, dm.S, dm.dffs, dm.d / div, elem, 16) ||
-                     !encode_tma_3d(&p.ws2, a.Ws2, dm.S, dm.d, dm.dffs / div, elem, p.rows3)))
+    if (dm.S > 0 && (!encode_tma_3d(&p.ws1, a.Ws1, dm.S, dm.dffs, dm.d / div, elem, 128) ||
+                     !encode_tma_3d(&p.ws2, a.Ws2, dm.S, dm.d, dm.dffs / div, elem, 128)))
         return cudaErrorInvalidValue;
     if (dm.dtype == MOE_BF16) return launch_mode<M_BF16>(p, plan.blocks, st);
     if (dm.dtype == MOE_FP8_E4M3_BLOCK) return launch_mode<M_FP8>(p, plan.blocks, st);
