@@ -40,6 +40,11 @@
 //   warps 0..3  epilogue (thread = row);   warps 4..7  token side: operand
 //   rows and all scales by cp.async;       (both: phase 1, the selection and
 //   the conversion of h)   warp 8  weights by TMA;   warp 9  MMA issue.
+// The weights stream past L2, so at every call the code itself comes from HBM:
+// a phase's first instructions cost as much as its first weights.  The role
+// loops therefore run both phases through the same code (measured: 172 KB of
+// code took 10 us to select the experts of one token and 7 us from there to
+// the first weights).
 // Every wait is bounded (common.cuh); after a wait gives up, the warps skip
 // the remaining work but keep meeting at the block's barriers.
 #include <cuda.h>
@@ -70,15 +75,15 @@ constexpr int OFF_GATE = OFF_IDX + MAX_T * 16 * 4;             // [16][16] float
 constexpr int OFF_MASK = OFF_GATE + MAX_T * 16 * 4;            // [256] tokens kept, per expert
 constexpr int OFF_KPACK = OFF_MASK + 256 * 4;                  // [256] 4 bits per token: its slot
 constexpr int OFF_ACT = OFF_KPACK + 256 * 8;                   // [256] experts reached, ascending
-constexpr int OFF_OUT = OFF_ACT + 256 * 4;                     // [16][128] fp32 output sums
+constexpr int OFF_COUNT = OFF_ACT + 256 * 4;                   // [256] slots that name the expert
+constexpr int OFF_OUT = OFF_COUNT + 256 * 4;                   // [16][128] fp32 sums of a tile
 constexpr int OFF_BAR = OFF_OUT + MAX_T * 128 * 4;             // full, empty [MAX_SLOTS]; accf, acce [2]; drain
 constexpr int OFF_MISC = OFF_BAR + (2 * MAX_SLOTS + 5) * 8;    // abort flag, n_active, tmem address, last flag, 8 warp counts
 constexpr int OFF_RING = (OFF_MISC + 64 + 1023) & ~1023;
-constexpr int RING_BYTES = 207 * 1024;
+constexpr int RING_BYTES = 206 * 1024;
 constexpr int SMEM_ALLOC = OFF_RING + RING_BYTES + 1024;
 static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
 static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
-static_assert(RING_BYTES >= MAX_T * 256 * 4 + 256 * 4, "the router's probabilities fit the ring's memory");
 static_assert(SF_COL0 + 2 * SF_COLS <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
 
 // grid-wide counters in the workspace, zero between launches
@@ -100,6 +105,7 @@ struct __align__(64) FewParams {
     int32_t* status;
     uint32_t* ctr;
     float* part;                  // (ks, T, E) partial logits
+    float* prob;                  // (T, 256) softmax of the logits
     uint8_t* xq;                  // x in operand form (bf16: x itself)
     uint8_t* xs;                  // its scales: FP8 a word per 128 columns, MXFP4 a byte per 32
     float* h32;                   // fp32 h: (T K, dff), then (S T, dffs)
@@ -123,8 +129,9 @@ template <> struct Form<M_FP4> { static constexpr int KP = 256, P = PLANES, SF =
 
 __host__ __device__ constexpr int round16(int v) { return (v + 15) & ~15; }
 
-__device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); }
+__device__ __forceinline__ void bar_general() { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); }
 
+__device__ __forceinline__ void bar_tokens() { asm volatile("bar.sync 3, %0;" :: "n"(EPI) : "memory"); }
 __device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 2, %0;" :: "n"(EPI) : "memory"); }
 
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
@@ -152,8 +159,8 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
 // 128 consecutive values of row `row` (a token of x, a slot of h) starting at
 // column col, four per lane, into the operand form of rows of k columns.
 template <int MODE>
-__device__ __forceinline__ void store_block(float (&v)[4], uint8_t* q, uint8_t* scales, size_t row, int k, int col,
-                                            int lane) {
+__device__ __noinline__ void store_block(float4 v4, uint8_t* q, uint8_t* scales, size_t row, int k, int col, int lane) {
+    float v[4] = {v4.x, v4.y, v4.z, v4.w};
     if (MODE == M_FP8) {
         // as the dispatch quantiser: fmaxf does not count a NaN
         float a = 0.f;
@@ -177,7 +184,7 @@ __device__ __forceinline__ void store_block(float (&v)[4], uint8_t* q, uint8_t* 
         const float inv = mxfp4_inv_scale(b == 255u ? 127u : b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= inv;
-#pragma unroll
+#pragma unroll 1
         for (int pl = 0; pl < PLANES; ++pl) {
             // scale exponents b, b - 2, b - 5, b - 8, b - 11; a plane below the
             // smallest scale holds nothing
@@ -211,29 +218,31 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Ctx& 
     return mbar_wait_bounded(bar, parity, c.abort_flag, c.p.status, kWaitNs);
 }
 
-// All consumer threads of all blocks.  Writes before it are visible to reads
+// The general warps of all blocks.  Writes before it are visible to reads
 // (through L2) after it.
-__device__ void grid_barrier(const Ctx& c, int which) {
-    bar_consumers();
-    if (c.tid == 0) {
-        uint32_t* ctr = c.p.ctr + CTR_BAR + which;
+__device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* status, volatile int* abort_flag, int tid) {
+    bar_general();
+    if (tid == 0) {
+        uint32_t* ctr = ctrs + CTR_BAR + which;
         __threadfence();
         atomicAdd(ctr, 1u);
-        if (*c.abort_flag) atomicExch(c.p.ctr + CTR_ABORT, 1u);
-        const uint64_t t0 = global_timer_ns();
-        for (uint32_t it = 1; !*c.abort_flag && ld_acquire(ctr) < gridDim.x; ++it) {
-            if ((it & 63u) == 0) {
-                if (ld_acquire(c.p.ctr + CTR_ABORT)) *c.abort_flag = 1;
-                else if (global_timer_ns() - t0 > kWaitNs) {
-                    *c.abort_flag = 1;
-                    set_device_status(c.p.status, MOE_DEV_TIMEOUT);
-                    atomicExch(c.p.ctr + CTR_ABORT, 1u);
+        if (*abort_flag) atomicExch(ctrs + CTR_ABORT, 1u);
+        uint64_t t0 = 0;
+        for (uint32_t it = 1; !*abort_flag && ld_acquire(ctr) < gridDim.x; ++it) {
+            if ((it & 255u) == 0) {
+                const uint64_t now = global_timer_ns();
+                if (t0 == 0) t0 = now;
+                if (ld_acquire(ctrs + CTR_ABORT)) *abort_flag = 1;
+                else if (now - t0 > kWaitNs) {
+                    *abort_flag = 1;
+                    set_device_status(status, MOE_DEV_TIMEOUT);
+                    atomicExch(ctrs + CTR_ABORT, 1u);
                 }
             }
         }
         __threadfence();
     }
-    bar_consumers();
+    bar_general();
 }
 
 // ---------------------------------------------------------------- jobs
@@ -253,31 +262,32 @@ struct Job {
     int block0, block1;
 };
 
-// Row of the operand arrays of x (phase 2) or h (phase 3) for token t.
-template <int PHASE>
-__device__ __forceinline__ int token_row(const Ctx& c, const Job& j, int t) {
-    if (PHASE == 2) return t;
+// Row of h for token t of a job.
+__device__ __forceinline__ int h_row(const Ctx& c, const Job& j, int t) {
     return j.shared ? j.mat * c.p.T + t : t * c.p.K + (static_cast<int>(j.kpack >> (4 * t)) & 15);
 }
 
 // This block's share of a phase's slots, job by job.  Phase 2: matrix by
 // matrix, its tiles, their slots of K = d.  Phase 3: tile by tile, the shared
 // experts' slots, then those of the experts reached.
-template <int MODE, int PHASE>
+template <int MODE>
 struct Jobs {
     const Ctx& c;
-    int at, end, all, parts;
+    const bool third;     // phase 3
+    int at, end;
+    int each, extra;      // slots of a block; the first `extra` blocks have one more
     int ss, sr;           // slots of a shared, a routed matrix per tile
     int ts, tr;           // phase 2: tiles of a shared, a routed matrix
     int tile;             // phase 3: slots of a tile
     static __device__ __forceinline__ int slots_of(int k) { return (k + NP * Form<MODE>::KP - 1) / (NP * Form<MODE>::KP); }
-    __device__ __forceinline__ Jobs(const Ctx& c_, int n_active) : c(c_) {
+    __device__ __forceinline__ Jobs(const Ctx& c_, int phase, int n_active) : c(c_), third(phase == 3) {
         const FewParams& p = c.p;
-        if (PHASE == 2) {
+        int all;
+        if (!third) {
             ss = sr = slots_of(p.d);
             ts = (p.dffs + 127) / 128;
             tr = (p.dff + 127) / 128;
-            tile = 0;
+            tile = 1;
             all = (p.S * ts + n_active * tr) * sr;
         } else {
             ss = slots_of(p.dffs);
@@ -288,20 +298,22 @@ struct Jobs {
         }
         // with fewer slots than blocks the last blocks have none, so that every
         // block between a tile's first and last has some of it
-        parts = min(static_cast<int>(gridDim.x), all);
-        const int b = min(static_cast<int>(blockIdx.x), parts);
-        at = static_cast<int>(static_cast<long long>(all) * b / parts);
-        end = static_cast<int>(static_cast<long long>(all) * min(b + 1, parts) / parts);
+        const int b = blockIdx.x;
+        each = all / static_cast<int>(gridDim.x);
+        extra = all - each * static_cast<int>(gridDim.x);
+        at = b * each + min(b, extra);
+        end = at + each + (b < extra ? 1 : 0);
     }
     // the block that has slot u
     __device__ __forceinline__ int block_of(int u) const {
-        return static_cast<int>((static_cast<long long>(u + 1) * parts - 1) / all);
+        const int v = u - extra * (each + 1);
+        return v < 0 ? u / (each + 1) : extra + v / each;
     }
     __device__ __forceinline__ bool next(Job& j) {
         if (at >= end) return false;
         const FewParams& p = c.p;
-        int u = at, first = 0, m;
-        if (PHASE == 3) {
+        int u = at, first = 0;
+        if (third) {
             j.row0 = u / tile * 128;
             first = u / tile * tile;
             u -= first;
@@ -310,10 +322,10 @@ struct Jobs {
         j.shared = u < n_shared;
         if (!j.shared) u -= n_shared;
         const int per = j.shared ? ss : sr, tiles = j.shared ? ts : tr;
-        const int run = u / per, s0 = u % per;                 // (matrix, tile), first slot of it
-        m = run / tiles;
-        if (PHASE == 2) {
-            j.row0 = run % tiles * 128;
+        const int run = u / per, s0 = u - run * per;           // (matrix, tile), first slot of it
+        const int m = run / tiles;
+        if (!third) {
+            j.row0 = (run - m * tiles) * 128;
             first = at - s0;
         }
         const int take = min(per - s0, end - at);
@@ -321,12 +333,12 @@ struct Jobs {
         j.mask = j.shared ? (1u << p.T) - 1u : reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK)[j.mat];
         j.kpack = j.shared ? 0 : reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK)[j.mat];
         const int inner = j.shared ? p.dffs : p.dff;
-        j.n = PHASE == 2 ? inner : p.d;
-        j.k = PHASE == 2 ? p.d : inner;
+        j.n = third ? p.d : inner;
+        j.k = third ? inner : p.d;
         j.p0 = s0 * NP;
         j.p1 = min((s0 + take) * NP, (j.k + Form<MODE>::KP - 1) / Form<MODE>::KP);
         at += take;
-        const int last = first + (PHASE == 2 ? per : tile) - 1;
+        const int last = first + (third ? tile : per) - 1;
         j.ends = at == end || at > last;
         j.block0 = block_of(first);
         j.block1 = block_of(last);
@@ -377,16 +389,16 @@ __device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const C
 // (The tensor core reads them through the async proxy: the MMA thread, which
 // has nothing else in flight, makes the proxy fence.  Made here it would wait
 // for the copies just issued: measured 1000 cycles a piece.)
-template <int MODE, int PHASE>
-__device__ __forceinline__ void load_tokens(const Ctx& c, int n_active, const uint8_t* base, const uint8_t* bscales,
-                                            size_t shared_elems, const void* ws, const void* ws_shared, Ring& ring,
-                                            bool& ok) {
+template <int MODE>
+__device__ __forceinline__ void load_tokens(const Ctx& c, int phase, int n_active, size_t h_shared, Ring& ring, bool& ok) {
     constexpr int P = Form<MODE>::P, KP = Form<MODE>::KP;
+    const FewParams& p = c.p;
+    const bool third = phase == 3;
     const int i = c.tid - EPI;
     const int q = i & 7;                                       // 16-byte chunk of a row's 128 bytes
     const int word = 16 * (i & 31) + 4 * (i >> 5);             // row i's word in 512 bytes of scales
     const int row_bytes = rows_bytes<MODE>(c), sf_at = scales_at<MODE>(c);
-    Jobs<MODE, PHASE> jobs(c, n_active);
+    Jobs<MODE> jobs(c, phase, n_active);
     Job j;
     while (ok && jobs.next(j)) {
         const int rows = __popc(j.mask) * P;
@@ -394,17 +406,18 @@ __device__ __forceinline__ void load_tokens(const Ctx& c, int n_active, const ui
         const size_t pitch = MODE == M_BF16 ? 2 * static_cast<size_t>(j.k) : MODE == M_FP8 ? j.k : j.k / 2;
         const int kq = MODE == M_FP8 ? j.k / 128 * 4 : j.k / 32;   // and of its scales
         // shared experts' rows of h follow the routed ones, at their own width
-        const uint8_t* data = base;
-        const uint8_t* sc = bscales;
-        if (PHASE == 3 && j.shared) {
-            const size_t skip = shared_elems * P;
+        const uint8_t* data = third ? p.hq : p.xq;
+        const uint8_t* sc = third ? p.hs : p.xs;
+        if (third && j.shared) {
+            const size_t skip = h_shared * P;
             data += MODE == M_BF16 ? 2 * skip : MODE == M_FP8 ? skip : skip / 2;
             sc += MODE == M_FP8 ? skip / 128 * 4 : skip / 32;
         }
         auto operand_row = [&](int n) {                        // of column n
             uint32_t m = j.mask;
             for (int z = n / P; z > 0; --z) m &= m - 1;
-            return static_cast<size_t>(token_row<PHASE>(c, j, __ffs(m) - 1) * P + n % P);
+            const int t = __ffs(m) - 1;
+            return static_cast<size_t>((third ? h_row(c, j, t) : t) * P + n % P);
         };
         const uint8_t* src[P];                                 // 16 rows at a time, 16 P in all
 #pragma unroll
@@ -417,7 +430,7 @@ __device__ __forceinline__ void load_tokens(const Ctx& c, int n_active, const ui
         if (MODE != M_BF16) {
             if (i < rows) bs = sc + operand_row(i) * kq;
             if (j.row0 + i < j.n) {
-                const uint8_t* w = static_cast<const uint8_t*>(j.shared ? ws_shared : ws);
+                const uint8_t* w = static_cast<const uint8_t*>(third ? (j.shared ? p.ws2s : p.w2s) : (j.shared ? p.ws1s : p.w1s));
                 as = MODE == M_FP8 ? w + (static_cast<size_t>(j.mat) * (j.n / 128) + j.row0 / 128) * kq
                                    : w + (static_cast<size_t>(j.mat) * j.n + j.row0 + i) * kq;
             }
@@ -631,19 +644,14 @@ __device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mas
 
 // ---------------------------------------------------------------- phase 1
 
+// Router slices are at most 14 x 128 columns: a warp holds an expert's slice
+// in registers (14 float4 a lane, one round of loads) and runs the tokens past
+// it.
+constexpr int SLICE_PIECES = 14;
+
 template <int MODE>
 __device__ __forceinline__ void router_and_x(const Ctx& c) {
     const FewParams& p = c.p;
-    if (MODE != M_BF16) {
-        const int nb = p.d / 128;
-        for (int i = blockIdx.x * CW + c.warp; i < p.T * nb; i += gridDim.x * CW) {
-            const int t = i / nb, b = i % nb;
-            const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.d + b * 128) + c.lane);
-            float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
-            store_block<MODE>(v, p.xq, p.xs, t, p.d, b * 128, c.lane);
-        }
-    }
     // a block has one slice of d and a share of the experts; it stages the
     // tokens' slices in the ring's memory
     const int sharers = gridDim.x / p.ks, who = blockIdx.x / p.ks, ks = blockIdx.x % p.ks;
@@ -651,37 +659,47 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
     if (who < sharers) {
         const int e0 = p.E * who / sharers, e1 = p.E * (who + 1) / sharers;
         const int k0 = ks * p.slice, len = min(p.slice, p.d - k0);       // multiples of 64
-        for (int i = c.tid; i < p.T * (len / 8); i += CT) {
-            const int t = i / (len / 8), q = i % (len / 8);
-            reinterpret_cast<uint4*>(xsm + t * p.slice)[q] =
-                __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.d + k0) + q);
+        const int rounds = (len + 127) / 128;                            // (zeros up to the last one's end)
+        for (int i = c.tid; i < p.T * rounds * 16; i += CT) {
+            const int t = i / (rounds * 16), q = i - t * rounds * 16;
+            reinterpret_cast<uint4*>(xsm + t * p.slice)[q] = 8 * q < len
+                ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.d + k0) + q) : make_uint4(0, 0, 0, 0);
         }
-        bar_consumers();
-        for (int e = e0 + c.warp; e < e1; e += CW) {
-            const float4* w = reinterpret_cast<const float4*>(p.W_r + static_cast<size_t>(e) * p.d + k0);
-            float acc[MAX_T] = {};
-#pragma unroll 4
-            for (int q = c.lane; q < len / 4; q += 32) {
-                const float4 wv = __ldg(w + q);
+        for (int e = e0 + c.warp; e < e0 + (e1 - e0 + CW - 1) / CW * CW; e += CW) {
+            float4 w[SLICE_PIECES];
+            const float4* src = reinterpret_cast<const float4*>(p.W_r + static_cast<size_t>(min(e, p.E - 1)) * p.d + k0);
 #pragma unroll
-                for (int t = 0; t < MAX_T; ++t) {
-                    if (t < p.T) {
-                        const uint2 xv = *reinterpret_cast<const uint2*>(xsm + t * p.slice + 4 * q);
-                        acc[t] = fmaf(__uint_as_float(xv.x << 16), wv.x, acc[t]);
-                        acc[t] = fmaf(__uint_as_float(xv.x & 0xFFFF0000u), wv.y, acc[t]);
-                        acc[t] = fmaf(__uint_as_float(xv.y << 16), wv.z, acc[t]);
-                        acc[t] = fmaf(__uint_as_float(xv.y & 0xFFFF0000u), wv.w, acc[t]);
+            for (int i = 0; i < SLICE_PIECES; ++i)
+                w[i] = 32 * i + c.lane < len / 4 ? __ldg(src + 32 * i + c.lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e < e0 + CW) bar_general();                              // the slices of x are there
+            if (e >= e1) continue;
+#pragma unroll 1
+            for (int t = 0; t < p.T; ++t) {
+                float acc = 0.f;
+#pragma unroll
+                for (int i = 0; i < SLICE_PIECES; ++i) {
+                    if (i < rounds) {
+                        const uint2 xv = *reinterpret_cast<const uint2*>(xsm + t * p.slice + 4 * (32 * i + c.lane));
+                        acc = fmaf(__uint_as_float(xv.x << 16), w[i].x, acc);
+                        acc = fmaf(__uint_as_float(xv.x & 0xFFFF0000u), w[i].y, acc);
+                        acc = fmaf(__uint_as_float(xv.y << 16), w[i].z, acc);
+                        acc = fmaf(__uint_as_float(xv.y & 0xFFFF0000u), w[i].w, acc);
                     }
                 }
-            }
 #pragma unroll
-            for (int t = 0; t < MAX_T; ++t) {
-                if (t >= p.T) break;
-                float v = acc[t];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (c.lane == t) p.part[(static_cast<size_t>(ks) * p.T + t) * p.E + e] = v;
+                for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                if (c.lane == 0) p.part[(static_cast<size_t>(ks) * p.T + t) * p.E + e] = acc;
             }
+        }
+    }
+    if (MODE != M_BF16) {
+        const int nb = p.d / 128;
+        for (int i = blockIdx.x * CW + c.warp; i < p.T * nb; i += gridDim.x * CW) {
+            const int t = i / nb, b = i % nb;
+            const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.d + b * 128) + c.lane);
+            store_block<MODE>(make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)),
+                              p.xq, p.xs, t, p.d, b * 128, c.lane);
         }
     }
 }
@@ -694,10 +712,10 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return max(b & 0x80000000u ? ~b : b | 0x80000000u, 1u);
 }
 
-// Top-K, gates and the list of experts reached, by every block for itself;
-// the last block also writes the routing outputs and the balance statistics.
-// Returns the number of experts reached (the same in every thread).
-__device__ int select_experts(const Ctx& c) {
+// Top-K, gates and the list of experts reached, by every block for itself (the
+// last block also keeps the probabilities, for balance()).  The number of
+// experts reached goes to the block's misc words.
+__device__ __forceinline__ void select_experts(const Ctx& c) {
     const FewParams& p = c.p;
     int* idx_s = reinterpret_cast<int*>(c.smem + OFF_IDX);
     float* gate_s = reinterpret_cast<float*>(c.smem + OFF_GATE);
@@ -705,20 +723,23 @@ __device__ int select_experts(const Ctx& c) {
     uint64_t* kpack_s = reinterpret_cast<uint64_t*>(c.smem + OFF_KPACK);
     int* act_s = reinterpret_cast<int*>(c.smem + OFF_ACT);
     int* misc = reinterpret_cast<int*>(c.smem + OFF_MISC);
-    float* prob_s = reinterpret_cast<float*>(c.smem + OFF_RING);      // [T][256], last block only
     const bool writer = blockIdx.x == gridDim.x - 1;
     for (int t = c.warp; t < p.T; t += CW) {
         float l[8];
         uint32_t key[8];
         float top = -INFINITY;
-        const float* part = p.part + static_cast<size_t>(t) * p.E + c.lane;
+        const float* part = p.part + static_cast<size_t>(t) * p.E;
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] = 0.f;
-#pragma unroll 4
+        // every load of a round is issued before the first is used (experts past
+        // the last one read the last one's)
+#pragma unroll 2
         for (int s = 0; s < p.ks; ++s) {
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (32 * i + c.lane < p.E) l[i] += __ldcg(part + static_cast<size_t>(s) * p.T * p.E + 32 * i);
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + s * p.T * p.E + min(32 * i + c.lane, p.E - 1));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l[i] += v[i];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -740,8 +761,9 @@ __device__ int select_experts(const Ctx& c) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (writer) {
+            const float inv = 1.f / sum;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) prob_s[t * 256 + 32 * i + c.lane] = l[i] / sum;
+            for (int i = 0; i < 8; ++i) p.prob[t * 256 + 32 * i + c.lane] = l[i] * inv;
         }
         float chosen = 0.f, mine = 0.f;
         for (int k = 0; k < p.K; ++k) {
@@ -764,7 +786,7 @@ __device__ int select_experts(const Ctx& c) {
     }
     mask_s[c.tid] = 0;
     kpack_s[c.tid] = 0;
-    bar_consumers();
+    bar_general();
     // the slots of every expert as bits (a token has at most one)
     {
         const int t = c.tid / 16, k = c.tid % 16;
@@ -774,11 +796,12 @@ __device__ int select_experts(const Ctx& c) {
             atomicOr(reinterpret_cast<unsigned long long*>(kpack_s + e), static_cast<unsigned long long>(k) << (4 * t));
         }
     }
-    bar_consumers();
+    bar_general();
     // one thread per expert: those within the capacity
     const int e = c.tid;
     uint32_t mask = mask_s[e];
     const int count = __popc(mask);
+    reinterpret_cast<int*>(c.smem + OFF_COUNT)[e] = count;
     if (p.capacity >= 0 && count > p.capacity) {
         uint32_t keep = 0;
         int left = p.capacity;
@@ -793,7 +816,7 @@ __device__ int select_experts(const Ctx& c) {
     }
     const uint32_t votes = __ballot_sync(0xffffffffu, mask != 0);
     if (c.lane == 0) misc[4 + c.warp] = __popc(votes);
-    bar_consumers();
+    bar_general();
     int base = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < CW; ++w) {
@@ -803,36 +826,36 @@ __device__ int select_experts(const Ctx& c) {
     }
     if (mask) act_s[base + __popc(votes & ((1u << c.lane) - 1u))] = e;
     if (c.tid == 0) misc[1] = total;
-    if (writer) {
-        for (int i = c.tid; i < p.T * p.K; i += CT) {
-            if (p.topk_idx) p.topk_idx[i] = idx_s[(i / p.K) * 16 + i % p.K];
-            if (p.gates) p.gates[i] = gate_s[(i / p.K) * 16 + i % p.K];
-        }
-        float* prod = prob_s + MAX_T * 256;
-        float fp = 0.f;
-        if (e < p.E) {
-            float P = 0.f;
-            for (int t = 0; t < p.T; ++t) P += prob_s[t * 256 + e];
-            P /= p.T;
-            const float f = static_cast<float>(count) / static_cast<float>(p.T * p.K);
-            p.P[e] = P;
-            p.f[e] = f;
-            if (p.counts) p.counts[e] = count;
-            fp = f * P;
-        }
-        prod[e] = fp;
-        bar_consumers();
-        if (c.warp == 0) {
-            float v = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v += prod[8 * c.lane + i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (c.lane == 0) *p.loss = p.alpha * p.E * v;
-        }
-        bar_consumers();
+}
+
+// The routing outputs and the balance statistics, by the token-side threads of
+// the last block once they have no copies left to make.
+__device__ __forceinline__ void balance(const Ctx& c) {
+    const FewParams& p = c.p;
+    const int i = c.tid - EPI;
+    for (int s = i; s < p.T * p.K; s += EPI) {
+        const int at = s / p.K * 16 + s % p.K;
+        if (p.topk_idx) p.topk_idx[s] = reinterpret_cast<const int*>(c.smem + OFF_IDX)[at];
+        if (p.gates) p.gates[s] = reinterpret_cast<const float*>(c.smem + OFF_GATE)[at];
     }
-    return total;
+    float sum = 0.f;
+    for (int e = i; e < p.E; e += EPI) {
+        float P = 0.f;
+        for (int t = 0; t < p.T; ++t) P += __ldcg(p.prob + t * 256 + e);
+        P /= static_cast<float>(p.T);
+        const int count = reinterpret_cast<const int*>(c.smem + OFF_COUNT)[e];
+        const float f = static_cast<float>(count) / static_cast<float>(p.T * p.K);
+        p.P[e] = P;
+        p.f[e] = f;
+        if (p.counts) p.counts[e] = count;
+        sum += f * P;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float* red = reinterpret_cast<float*>(c.smem + OFF_MISC) + 4;         // the selection's counts
+    if (c.lane == 0) red[c.warp - 4] = sum;
+    bar_tokens();
+    if (i == 0) *p.loss = p.alpha * p.E * (red[0] + red[1] + red[2] + red[3]);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -878,10 +901,10 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         Ring ring;
         bool ok = *c.abort_flag == 0;
         Job j;
-        for (Jobs<MODE, 2> jobs(c, n_active); ok && jobs.next(j);)
-            ok = load_weights<MODE>(c, j, j.shared ? &p.ws1 : &p.w1, ring);
-        for (Jobs<MODE, 3> jobs(c, n_active); ok && jobs.next(j);)
-            ok = load_weights<MODE>(c, j, j.shared ? &p.ws2 : &p.w2, ring);
+#pragma unroll 1
+        for (int phase = 2; phase <= 3; ++phase)
+            for (Jobs<MODE> jobs(c, phase, n_active); ok && jobs.next(j);)
+                ok = load_weights<MODE>(c, j, phase == 2 ? (j.shared ? &p.ws1 : &p.w1) : (j.shared ? &p.ws2 : &p.w2), ring);
         // a block that gave up leaves its copies the time to land before it
         // gives its memory back (their barriers may never complete, since the
         // token side stopped arriving)
@@ -897,8 +920,10 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
             MmaState st;
             bool ok = *c.abort_flag == 0;
             Job j;
-            for (Jobs<MODE, 2> jobs(c, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
-            for (Jobs<MODE, 3> jobs(c, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
+#pragma unroll 1
+            for (int phase = 2; phase <= 3; ++phase)
+                for (Jobs<MODE> jobs(c, phase, n_active); ok && jobs.next(j);)
+                    ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
             if (!ok && st.issued) {
                 umma_commit(drain);
                 volatile int no_abort = 0;
@@ -908,82 +933,81 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         __syncwarp();
     } else {
         router_and_x<MODE>(c);
-        grid_barrier(c, 0);
-        const int n_active = select_experts(c);
-        fence_proxy_async_smem();                               // phase 1 and the selection used the ring's memory
+        grid_barrier(p.ctr, 0, p.status, c.abort_flag, c.tid);
+        select_experts(c);
+        fence_proxy_async_smem();                               // phase 1 used the ring's memory
         __syncthreads();
-        const int slots_h = p.T * p.K;                          // rows of routed h
-        const size_t h_shared = static_cast<size_t>(slots_h) * p.dff;
-        const bool epilogue = c.warp < 4;
-        const int my_row = c.tid;                               // epilogue: this thread's row of a tile
-        float* sums = reinterpret_cast<float*>(smem + OFF_OUT) + my_row;           // [t * 128]
-        Ring ring;
-        int jobs_read = 0;
-        bool ok = *c.abort_flag == 0;
-        Job j;
-        if (epilogue) {
-            for (Jobs<MODE, 2> jobs(c, n_active); jobs.next(j);) {
-                const bool in = j.row0 + my_row < j.n;
-                const float bias = in ? __ldg((j.shared ? p.bs1 : p.b1) + static_cast<size_t>(j.mat) * j.n + j.row0 + my_row)
-                                      : 0.f;
-                read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) { sums[t * 128] = v; });
-                if (!combine(c, j, j.mask, sums) || !in) continue;
-                const size_t base = j.shared ? h_shared : 0;
-                for (uint32_t m = j.mask; m; m &= m - 1) {
-                    const int t = __ffs(m) - 1;
-                    const float h = silu_fast(sums[t * 128] + bias);
-                    const size_t at = base + static_cast<size_t>(token_row<3>(c, j, t)) * j.n + j.row0 + my_row;
-                    if (MODE == M_BF16) reinterpret_cast<__nv_bfloat16*>(p.hq)[at] = __float2bfloat16_rn(h);
-                    else p.h32[at] = h;
-                }
-            }
-        } else {
-            load_tokens<MODE, 2>(c, n_active, p.xq, p.xs, 0, p.w1s, p.ws1s, ring, ok);
-        }
-        grid_barrier(c, 1);
+        const int n_active = misc[1];
         const int* idx_s = reinterpret_cast<const int*>(smem + OFF_IDX);
         const float* gate_s = reinterpret_cast<const float*>(smem + OFF_GATE);
         const uint32_t* mask_s = reinterpret_cast<const uint32_t*>(smem + OFF_MASK);
-        if (MODE != M_BF16) {
-            // a warp per 128 values of h that phase 3 reads; a slot over the capacity has none
-            constexpr int P = Form<MODE>::P;
-            const int nr = p.dff / 128, ns = p.dffs / 128;
-            const int routed = slots_h * nr, all = routed + p.S * p.T * ns;
-            uint8_t* hq_shared = p.hq + h_shared * P / (MODE == M_FP4 ? 2 : 1);
-            uint8_t* hs_shared = p.hs + (MODE == M_FP4 ? h_shared * P / 32 : h_shared / 128 * 4);
-            for (int i = blockIdx.x * CW + c.warp; i < all; i += gridDim.x * CW) {
-                const bool sh = i >= routed;
-                const int u = sh ? i - routed : i, nb = sh ? ns : nr, row = u / nb, col = u % nb * 128;
-                if (!sh && !(mask_s[idx_s[row / p.K * 16 + row % p.K]] >> (row / p.K) & 1u)) continue;
-                const int k = sh ? p.dffs : p.dff;
-                const float4 q = __ldcg(reinterpret_cast<const float4*>(
-                    p.h32 + (sh ? h_shared : 0) + static_cast<size_t>(row) * k + col) + c.lane);
-                float v[4] = {q.x, q.y, q.z, q.w};
-                store_block<MODE>(v, sh ? hq_shared : p.hq, sh ? hs_shared : p.hs, row, k, col, c.lane);
+        const int slots_h = p.T * p.K;                          // rows of routed h
+        const size_t h_shared = static_cast<size_t>(slots_h) * p.dff;
+        float* sums = reinterpret_cast<float*>(smem + OFF_OUT) + c.tid;            // epilogue: [t * 128]
+        Ring ring;
+        int jobs_read = 0;
+        bool ok = *c.abort_flag == 0;
+#pragma unroll 1
+        for (int phase = 2; phase <= 3; ++phase) {
+            const bool third = phase == 3;
+            if (third) {
+                grid_barrier(p.ctr, 1, p.status, c.abort_flag, c.tid);
+                if (MODE != M_BF16) {
+                    // h in operand form, a warp per 128 values that phase 3
+                    // reads; a slot over the capacity has none
+                    constexpr int P = Form<MODE>::P;
+                    const int nr = p.dff / 128, ns = p.dffs / 128;
+                    const int routed = slots_h * nr, blocks = routed + p.S * p.T * ns;
+                    uint8_t* hq_shared = p.hq + h_shared * P / (MODE == M_FP4 ? 2 : 1);
+                    uint8_t* hs_shared = p.hs + (MODE == M_FP4 ? h_shared * P / 32 : h_shared / 128 * 4);
+                    for (int i = blockIdx.x * CW + c.warp; i < blocks; i += gridDim.x * CW) {
+                        const bool sh = i >= routed;
+                        const int u = sh ? i - routed : i, nb = sh ? ns : nr, row = u / nb, col = u % nb * 128;
+                        const int t = row / p.K;
+                        if (!sh && !(mask_s[idx_s[t * 16 + row - t * p.K]] >> t & 1u)) continue;
+                        const int k = sh ? p.dffs : p.dff;
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                            p.h32 + (sh ? h_shared : 0) + static_cast<size_t>(row) * k + col) + c.lane);
+                        store_block<MODE>(v, sh ? hq_shared : p.hq, sh ? hs_shared : p.hs, row, k, col, c.lane);
+                    }
+                    grid_barrier(p.ctr, 2, p.status, c.abort_flag, c.tid);
+                }
+                ok = ok && *c.abort_flag == 0;
             }
-            grid_barrier(c, 2);
-        }
-        ok = ok && *c.abort_flag == 0;
-        if (!epilogue) {
-            load_tokens<MODE, 3>(c, n_active, p.hq, p.hs, h_shared, p.w2s, p.ws2s, ring, ok);
-        } else {
-            const uint32_t every = (1u << p.T) - 1u;
+            if (c.warp >= 4) {
+                load_tokens<MODE>(c, phase, n_active, h_shared, ring, ok);
+                if (third && blockIdx.x == gridDim.x - 1) balance(c);
+                continue;
+            }
             bool begins = true;
-            for (Jobs<MODE, 3> jobs(c, n_active); jobs.next(j);) {
+            Job j;
+            for (Jobs<MODE> jobs(c, phase, n_active); jobs.next(j);) {
                 if (begins) for (int t = 0; t < p.T; ++t) sums[t * 128] = 0.f;
                 begins = j.ends;
-                const int row = j.row0 + my_row;
-                const bool in = row < p.d;
-                // the block with a matrix's first piece adds its bias
-                const float bias = in && j.p0 == 0
-                    ? __ldg((j.shared ? p.bs2 : p.b2) + static_cast<size_t>(j.mat) * p.d + row) : 0.f;
+                const int row = j.row0 + c.tid;
+                const bool in = row < j.n;
+                // phase 3: the block with a matrix's first piece adds its bias
+                const float* biases = third ? (j.shared ? p.bs2 : p.b2) : (j.shared ? p.bs1 : p.b1);
+                const float bias = in && (!third || j.p0 == 0) ? __ldg(biases + static_cast<size_t>(j.mat) * j.n + row) : 0.f;
+                const bool gated = third && !j.shared;
+                const float inner = third ? bias : 0.f;
                 read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
-                    const float g = j.shared ? 1.f : gate_s[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)];
-                    sums[t * 128] = fmaf(g, v + bias, sums[t * 128]);
+                    const float g = gated ? gate_s[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)] : 1.f;
+                    sums[t * 128] = fmaf(g, v + inner, sums[t * 128]);
                 });
-                if (!j.ends || !combine(c, j, every, sums) || !in || !ok) continue;
-                for (int t = 0; t < p.T; ++t) {
+                const uint32_t tokens = third ? (1u << p.T) - 1u : j.mask;
+                if (!j.ends || !combine(c, j, tokens, sums) || !in || !ok) continue;
+                const size_t base = j.shared ? h_shared : 0;
+                for (uint32_t m = tokens; m; m &= m - 1) {
+                    const int t = __ffs(m) - 1;
                     float v = sums[t * 128];
+                    if (!third) {
+                        const float h = silu_fast(v + bias);
+                        const size_t at = base + static_cast<size_t>(h_row(c, j, t)) * j.n + row;
+                        if (MODE == M_BF16) reinterpret_cast<__nv_bfloat16*>(p.hq)[at] = __float2bfloat16_rn(h);
+                        else p.h32[at] = h;
+                        continue;
+                    }
                     const size_t at = static_cast<size_t>(t) * p.d + row;
                     if (p.passthrough) {
                         for (int k = 0; k < p.K; ++k)
@@ -1014,7 +1038,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 struct FewLayout {
-    size_t ctr, part, xq, xs, h32, hq, hs, sums, total;
+    size_t ctr, part, prob, xq, xs, h32, hq, hs, sums, total;
 };
 
 // blocks: as many as can find work, at most one per SM
@@ -1033,17 +1057,16 @@ FewPlan few_plan(const Dims& dm, int sms) {
     const long long s3 = reached * slots(dm.d, dm.dff) + dm.S * slots(dm.d, dm.dffs);
     const long long most = s2 > s3 ? s2 : s3;
     f.blocks = most < sms ? static_cast<int>(most) : sms;
-    // router: slices of d (multiples of 128 columns, at most 5120: 16 tokens'
-    // slice fills the ring's memory), as many as give each block at most one
-    // expert a warp
-    static_assert(MAX_T * 5120 * 2 <= RING_BYTES, "the staged slice of x fits the ring");
+    // router: slices of d (multiples of 128 columns), as many as give each
+    // block at most one expert a warp
+    static_assert(MAX_T * 128 * SLICE_PIECES * 2 <= RING_BYTES, "the staged slice of x fits the ring");
     int want = f.blocks * CW / dm.E;
     if (want > 16) want = 16;
     if (want > f.blocks) want = f.blocks;
     if (want < 1) want = 1;
     const int pieces = (dm.d + 127) / 128;
     int per = (pieces + want - 1) / want;
-    if (per > 40) per = 40;
+    if (per > SLICE_PIECES) per = SLICE_PIECES;
     f.slice = 128 * per;
     f.ks = (pieces + per - 1) / per;
     if (f.blocks < f.ks) f.blocks = f.ks;
@@ -1064,6 +1087,7 @@ FewLayout few_layout(const Dims& dm) {
     L.ctr = take((CTR_TILE + MAX_BLOCKS) * 4);
     // slices are at least 128 columns long, whatever the device's size
     L.part = take(static_cast<size_t>((dm.d + 127) / 128) * dm.T * dm.E * 4);
+    L.prob = take(static_cast<size_t>(dm.T) * 256 * 4);
     L.xq = take(q ? form(x) : 0);
     L.xs = take(scales(x));
     L.h32 = take(q ? h * 4 : 0);
@@ -1130,6 +1154,7 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     p.status = reinterpret_cast<int32_t*>(w);
     p.ctr = reinterpret_cast<uint32_t*>(w + L.ctr);
     p.part = reinterpret_cast<float*>(w + L.part);
+    p.prob = reinterpret_cast<float*>(w + L.prob);
     p.xq = dm.dtype == MOE_BF16 ? const_cast<uint8_t*>(static_cast<const uint8_t*>(a.x)) : w + L.xq;
     p.xs = w + L.xs;
     p.h32 = reinterpret_cast<float*>(w + L.h32);
