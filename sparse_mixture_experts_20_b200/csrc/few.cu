@@ -486,73 +486,98 @@ __device__ __forceinline__ void load_tokens(const Ctx& c, int phase, int n_activ
     }
 }
 
-// ---------------------------------------------------------------- MMA issue (one thread)
+// ---------------------------------------------------------------- MMA issue (one warp)
+//
+// The warp runs the loop as a whole and one elected lane issues: descriptors
+// and counters then are warp-uniform values (issued from a loop that only one
+// lane runs, an MMA cost about 200 cycles of moves, more than it takes).
 
 struct MmaState {
     Ring ring;
     int jobs = 0, slots = 0;
-    bool issued = false;
+    bool leader;
 };
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// wait() for a whole warp, which stays converged.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Ctx& c) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait(bar, parity, c));
+}
 
 template <int MODE>
 __device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, uint32_t tmem, uint64_t* accf, uint64_t* acce,
                                           MmaState& st) {
     const int buf = st.jobs & 1;
-    if (!wait(acce + buf, ((st.jobs >> 1) & 1) ^ 1u, c)) return false;
+    if (!wait_warp(acce + buf, ((st.jobs >> 1) & 1) ^ 1u, c)) return false;
     tc_fence_after();
     const uint32_t d = tmem + buf * ACC_COLS;
-    const uint32_t n = round16(__popc(j.mask) * Form<MODE>::P);
+    const uint32_t n = round16(__popc(__shfl_sync(0xffffffffu, j.mask, 0)) * Form<MODE>::P);
+    const uint32_t idesc = MODE == M_BF16 ? make_idesc(1, 128, n) : MODE == M_FP8 ? make_idesc_mxf8(128, n)
+                                                                                 : make_idesc_mxf4(n, 0);
+    const uint32_t idesc2 = MODE == M_FP4 ? make_idesc_mxf4(n, 2) : idesc;
+    const int p0 = __shfl_sync(0xffffffffu, j.p0, 0), p1 = __shfl_sync(0xffffffffu, j.p1, 0);
+    // MXFP4: the last piece of K may be a half
+    const int whole = MODE == M_FP4 ? __shfl_sync(0xffffffffu, j.k, 0) / Form<MODE>::KP : p1;
     const int row_bytes = rows_bytes<MODE>(c), sf_at = scales_at<MODE>(c);
-    for (int s = j.p0; s < j.p1; s += NP) {
-        if (!wait(c.full + st.ring.slot, st.ring.phase, c)) return false;
+    for (int s = p0; s < p1; s += NP) {
+        if (!wait_warp(c.full + st.ring.slot, st.ring.phase, c)) return false;
         fence_proxy_async_smem();                              // the token side was copied through the generic proxy
-        uint8_t* slot = slot_at(c, st.ring.slot);
         if (MODE != M_BF16 && st.slots >= 2) {
             // the MMAs that read this half of the scale columns two slots ago are done
             int q = st.ring.slot - 2;
             uint32_t ph = st.ring.phase;
             if (q < 0) { q += c.p.slots; ph ^= 1u; }
-            if (!wait(c.empty + q, ph, c)) return false;
+            if (!wait_warp(c.empty + q, ph, c)) return false;
         }
         tc_fence_after();
+        uint8_t* slot = slot_at(c, st.ring.slot);
+        const uint32_t sf0 = tmem + SF_COL0 + (st.slots & 1) * SF_COLS;
 #pragma unroll
         for (int r = 0; r < NP; ++r) {
-            if (s + r >= j.p1) break;
+            if (s + r >= p1) break;
             const uint64_t a = smem_desc_k_sw128(slot + r * PIECE_BYTES);
             const uint64_t b = smem_desc_k_sw128(slot + NP * PIECE_BYTES + r * row_bytes);
-            const uint32_t more = s + r > j.p0 ? 1u : 0u;
+            const uint32_t more = s + r > p0 ? 1u : 0u;
             const uint8_t* sf = slot + sf_at + r * Form<MODE>::SF;
-            const uint32_t t = tmem + SF_COL0 + (st.slots & 1) * SF_COLS + r * (SF_COLS / NP);
+            const uint32_t t = sf0 + r * (SF_COLS / NP);
             if (MODE == M_BF16) {
+                if (st.leader) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, make_idesc(1, 128, n), more | (k > 0));
-            } else if (MODE == M_FP8) {
-                tmem_cp_scales(t, sf);
-                tmem_cp_scales(t + 4, sf + 512);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_mxf8_bs(d, a + 2 * k, b + 2 * k, make_idesc_mxf8(128, n), t, t + 4, more | (k > 0));
-            } else {
-                const bool two = (s + r) * Form<MODE>::KP + 128 < j.k;
-                tmem_cp_scales(t, sf);
-                tmem_cp_scales(t + 8, sf + 1024);
-                if (two) {
-                    tmem_cp_scales(t + 4, sf + 512);
-                    tmem_cp_scales(t + 12, sf + 1536);
+                    for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, idesc, more | (k > 0));
                 }
+            } else if (MODE == M_FP8) {
+                if (st.leader) {
+                    tmem_cp_scales(t, sf);
+                    tmem_cp_scales(t + 4, sf + 512);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (k < 2 || two)
-                        umma_mxf4_bs(d, a + 2 * k, b + 2 * k, make_idesc_mxf4(n, 2 * (k & 1)), t + 4 * (k >> 1),
-                                     t + 8 + 4 * (k >> 1), more | (k > 0));
+                    for (int k = 0; k < 4; ++k) umma_mxf8_bs(d, a + 2 * k, b + 2 * k, idesc, t, t + 4, more | (k > 0));
+                }
+            } else {
+                if (st.leader) {
+                    tmem_cp_scales(t, sf);
+                    tmem_cp_scales(t + 8, sf + 1024);
+                    umma_mxf4_bs(d, a, b, idesc, t, t + 8, more);
+                    umma_mxf4_bs(d, a + 2, b + 2, idesc2, t, t + 8, 1);
+                    if (s + r < whole) {
+                        tmem_cp_scales(t + 4, sf + 512);
+                        tmem_cp_scales(t + 12, sf + 1536);
+                        umma_mxf4_bs(d, a + 4, b + 4, idesc, t + 4, t + 12, 1);
+                        umma_mxf4_bs(d, a + 6, b + 6, idesc2, t + 4, t + 12, 1);
+                    }
+                }
             }
         }
-        st.issued = true;
         ++st.slots;
-        umma_commit(c.empty + st.ring.slot);
+        if (st.leader) umma_commit(c.empty + st.ring.slot);
         st.ring.next(c.p.slots);
     }
-    umma_commit(accf + buf);
+    if (st.leader) umma_commit(accf + buf);
     ++st.jobs;
     return true;
 }
@@ -916,19 +941,17 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
     } else if (c.warp == W_MMA) {
         __syncthreads();
         const int n_active = misc[1];
-        if (c.lane == 0) {
-            MmaState st;
-            bool ok = *c.abort_flag == 0;
-            Job j;
+        MmaState st;
+        st.leader = elect_one();
+        bool ok = *c.abort_flag == 0;
+        Job j;
 #pragma unroll 1
-            for (int phase = 2; phase <= 3; ++phase)
-                for (Jobs<MODE> jobs(c, phase, n_active); ok && jobs.next(j);)
-                    ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
-            if (!ok && st.issued) {
-                umma_commit(drain);
-                volatile int no_abort = 0;
-                mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainNs);
-            }
+        for (int phase = 2; phase <= 3; ++phase)
+            for (Jobs<MODE> jobs(c, phase, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
+        if (!ok && st.slots && st.leader) {
+            umma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainNs);
         }
         __syncwarp();
     } else {
