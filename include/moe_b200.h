@@ -310,13 +310,14 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
  *                             cols/128); x and the hidden activation are
  *                             quantised to e4m3 per 128 columns
  *   dtype MOE_MXFP4           weights as moe_mxfp4_quantize writes them:
- *                             W1 (N_r, d_ff, d_model/2) bytes with W1_scales
- *                             (N_r, d_ff, d_model/32) bytes, W2 (N_r, d_model,
- *                             d_ff/2) with W2_scales (N_r, d_model, d_ff/32),
- *                             the shared experts likewise; x (bf16) and the
- *                             hidden activation are not quantised (held in
- *                             fp16 with a power-of-two scale per 128 columns)
- * In every mode x and out are bf16, biases and W_r fp32.
+ *                             W1 (N_r, d_ff, d_model/2) bytes, W2 (N_r,
+ *                             d_model, d_ff/2), with their scales in the order
+ *                             of moe_mxfp4_tile_scales; the shared experts
+ *                             likewise; x (bf16) and the hidden activation are
+ *                             not quantised: they enter as sums of five E2M1
+ *                             terms, within amax / 12288 of each 32 columns
+ * In every mode x and out are bf16, biases and W_r fp32; FP8 scales are powers
+ * of two.
  * Errors: MOE_ERR_UNSUPPORTED for MOE_F32, for T > MOE_FEW_MAX_TOKENS, and for
  * d_model or a d_ff that is not a multiple of 64 (bf16) or 128.
  * ws: moe_few_workspace_size() bytes, 256-byte aligned, zero-filled once by
@@ -358,6 +359,14 @@ MOE_EXPORT int moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, in
                                   uint8_t* codes, uint8_t* scales, void* stream);
 MOE_EXPORT int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
                                     void* out, int32_t dtype, void* stream);
+
+/* The scales (n_mats, rows, cols/32) of a stack of MXFP4 matrices in the order
+ * that moe_layer_forward_few streams: (n_mats, ceil(rows/128), cols/128, 512)
+ * bytes, where the four scale bytes of row r of a tile of 128 rows and of 128
+ * columns lie at 16 (r mod 32) + 4 (r div 32).  Rows past the end read as 2^0.
+ * cols a multiple of 128; pointers 16-byte aligned, not overlapping. */
+MOE_EXPORT int moe_mxfp4_tile_scales(const uint8_t* scales, int64_t n_mats, int32_t rows, int32_t cols,
+                                     uint8_t* tiled, void* stream);
 
 /* The grouped product of MXFP4 operands over caller-made segments (as
  * moe_expert_ffn_segments lays them out): for every row r of segment i,

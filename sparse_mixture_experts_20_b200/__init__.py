@@ -41,7 +41,7 @@ EXPORTED = (
     "moe_combine", "moe_balance_stats", "moe_layer_forward", "moe_selftest_wait_timeout",
     "moe_dispatch_noalloc", "moe_kernel_launches", "moe_backward_workspace_size", "moe_layer_backward",
     "moe_expert_ffn_segments", "moe_few_workspace_size", "moe_few_workspace_init", "moe_layer_forward_few",
-    "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_workspace_size",
+    "moe_mxfp4_quantize", "moe_mxfp4_dequantize", "moe_mxfp4_tile_scales", "moe_mxfp4_workspace_size",
     "moe_mxfp4_workspace_init", "moe_mxfp4_get_device_status", "moe_mxfp4_matmul",
 )
 
@@ -123,6 +123,7 @@ def lib() -> ctypes.CDLL:
             "moe_layer_forward_few": [cfgp] + [P] * 24,
             "moe_mxfp4_quantize": [P, i32, i64, i32, P, P, P],
             "moe_mxfp4_dequantize": [P, P, i64, i32, P, i32, P],
+            "moe_mxfp4_tile_scales": [P, i64, i32, i32, P, P],
             "moe_mxfp4_workspace_size": [shp, ctypes.POINTER(ctypes.c_size_t)],
             "moe_mxfp4_workspace_init": [shp, P, P],
             "moe_mxfp4_get_device_status": [shp, P, P, ctypes.POINTER(i32), i32],
@@ -310,8 +311,9 @@ def moe_few_workspace_init(cfg, ws, stream=None):
 def moe_layer_forward_few(cfg, x, W_r, logit_bias, W1, W1_scales, b1, W2, W2_scales, b2,
                           Ws1, Ws1_scales, bs1, Ws2, Ws2_scales, bs2, out, f, P, loss,
                           topk_idx, gates, counts, ws, stream=None):
-    """moe_layer_forward for at most MOE_FEW_MAX_TOKENS tokens, in one kernel (bf16, FP8 or MXFP4 experts);
-    ws: moe_few_workspace_size() bytes after moe_few_workspace_init."""
+    """moe_layer_forward for at most MOE_FEW_MAX_TOKENS tokens, in one kernel (bf16, FP8 or MXFP4 experts,
+    the last with scales from moe_mxfp4_tile_scales); ws: moe_few_workspace_size() bytes after
+    moe_few_workspace_init."""
     _check(lib().moe_layer_forward_few(ctypes.byref(cfg), _p(x), _p(W_r), _p(logit_bias), _p(W1), _p(W1_scales),
                                        _p(b1), _p(W2), _p(W2_scales), _p(b2), _p(Ws1), _p(Ws1_scales), _p(bs1),
                                        _p(Ws2), _p(Ws2_scales), _p(bs2), _p(out), _p(f), _p(P), _p(loss),
@@ -351,6 +353,18 @@ def moe_mxfp4_dequantize(codes, scales, out, stream=None):
            "moe_mxfp4_dequantize")
 
 
+def moe_mxfp4_tile_scales(scales, stream=None):
+    """The scales (n_mats, rows, cols / 32) uint8 of a stack of MXFP4 matrices, in the order that
+    moe_layer_forward_few streams."""
+    import torch
+    if scales.dim() != 3 or scales.dtype != torch.uint8 or scales.shape[1] < 1 or scales.shape[2] < 1:
+        raise ValueError("moe_mxfp4_tile_scales: scales are a uint8 stack (n_mats, rows, cols / 32)")
+    n, rows, cols = scales.shape[0], scales.shape[1], scales.shape[2] * 32
+    tiled = torch.empty((n, (rows + 127) // 128, cols // 128, 512), dtype=torch.uint8, device=scales.device)
+    _check(lib().moe_mxfp4_tile_scales(_p(scales), n, rows, cols, _p(tiled), _stream(stream)), "moe_mxfp4_tile_scales")
+    return tiled
+
+
 def make_mxfp4_shape(rows: int, n: int, k: int, n_mats: int = 1, n_seg: int = 1, activation: int = MOE_ACT_NONE,
                      out_dtype: int = MOE_BF16) -> moe_mxfp4_shape:
     return moe_mxfp4_shape(rows, n, k, n_mats, n_seg, activation, out_dtype)
@@ -388,7 +402,8 @@ class MoELayer:
     None where not used).  forward(x) runs moe_layer_forward on the current
     stream and returns (out, f, P, loss); forward_few(x) is the same layer
     through moe_layer_forward_few, for at most MOE_FEW_MAX_TOKENS tokens.  A
-    layer of MXFP4 experts has forward_few only.
+    layer of MXFP4 experts has forward_few only; its weights are codes and
+    scales as moe_mxfp4_quantize writes them, the scales tiled here once.
     """
 
     def __init__(self, cfg: moe_config, weights: dict, device="cuda"):
@@ -398,6 +413,10 @@ class MoELayer:
         self.device = torch.device(device)
         if cfg.dtype == MOE_MXFP4:
             self.ws = self._few_workspace()
+            self.w = dict(weights)
+            for k in ("W1_scales", "W2_scales", "Ws1_scales", "Ws2_scales"):
+                if weights.get(k) is not None:
+                    self.w[k] = moe_mxfp4_tile_scales(weights[k])
         else:
             self.ws = torch.empty(moe_workspace_size(cfg), dtype=torch.uint8, device=self.device)
             moe_workspace_init(cfg, self.ws)

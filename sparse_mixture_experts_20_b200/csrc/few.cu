@@ -2,44 +2,54 @@
 //
 // Decoding a few tokens is bound by the bytes of the experts they reach, so
 // the kernel is a stream of weight rows through every SM that nothing
-// interrupts: a warp loads pieces of 128 weight rows x 128 bytes by TMA into a
-// ring in shared memory, and tcgen05 multiplies them in place, the weights as
-// the 128-row operand and the tokens as a narrow one.  No thread touches a
-// weight; what the other warps do per piece is a few copies of the token side.
+// interrupts: pieces of 128 weight rows x 128 bytes go by TMA into a ring in
+// shared memory, and tcgen05 multiplies them in place, the weights as the
+// 128-row operand and the tokens as a narrow one.  No thread touches a weight,
+// and what a slot of the ring needs of the tokens is one or two bulk copies,
+// because phases 1 and 2 write x and h as the image that the tensor core reads.
 // One block per SM, launched cooperatively; the phases are separated by grid
 // barriers, and since weights do not depend on what the barriers wait for, the
 // ring keeps filling across them:
 //   1  router logits: (expert, slice of d) dot products in fp32, partial sums
-//      per slice; x into the operand form of the weights' type;
+//      per slice; the image of x;
 //   -- barrier; every block then selects the top-K of all tokens for itself
 //      (slices added in order) and builds the list of experts reached;
-//   2  h = SiLU(W1 x + b1), written per (token, slot);
-//   -- barrier; FP8 and MXFP4: h into the operand form, barrier;
+//   2  h = SiLU(W1 x + b1); bf16: straight into its image;
+//   -- barrier; FP8 and MXFP4: the image of h, barrier;
 //   3  out = sum over the experts of gate * (W2 h + b2), shared experts
 //      included.
 // Phases 2 and 3 are one sequence each of tiles of 128 result rows (phase 2:
 // of every expert's W1; phase 3: of the output, through every expert's W2),
-// each a run of slots (two pieces of K).  Every block takes the same number of
-// slots; a tile that crosses a block boundary is summed from its blocks' parts,
-// in block order, by whichever of them finishes last.
+// each a run of slots (two pieces of K), cut into a large share for every
+// block and, where that is long, small ones that the blocks take as they get to
+// them: SMs do not stream at the same speed (on B200 a quarter of them about
+// 12 % slower, GPC by GPC).  A tile that crosses a border between shares is
+// summed from the shares' parts, in order, by whichever block finishes last:
+// who takes a share changes nothing in the sums.
 //
 // Operand forms (products exact, sums in fp32):
 //   bf16   weights, x and h in bf16 (kind::f16);
 //   FP8    e4m3 (kind::mxf8f6f4.block_scale); x and h quantised to e4m3 per 128
-//          columns; all scales are powers of two and go to the tensor core;
-//   MXFP4  packed E2M1 with its E8M0 scales (kind::mxf4.block_scale).  x and h
-//          are not quantised: per 32 columns they are split into five E2M1
-//          planes, each the nearest E2M1 value of what the planes before it
-//          left, at scales s, s/4, s/32, s/256, s/2048.  A plane's remainder is
-//          at most half of the step at its largest magnitude (1, then 1/2 of
-//          the next plane's unit), so the five stand for the value to within
-//          s / 4096 <= amax / 12288.  A token is then five columns, which the
-//          tensor core has to spare.
+//          columns; all scales are powers of two and go to the tensor core.  A
+//          tile's weight scale is one number for 128 columns of K: tensor
+//          memory keeps eight "uniform" sets of scale columns, by exponent
+//          modulo 8, and an MMA names the one it needs;
+//   MXFP4  packed E2M1 with its E8M0 scales (kind::mxf4.block_scale), which lie
+//          tiled in the order that tcgen05.cp reads.  x and h are not
+//          quantised: per 32 columns they are split into five E2M1 planes,
+//          each the nearest E2M1 value of what the planes before it left, at
+//          scales s, s/4, s/32, s/256, s/2048.  A plane's remainder is at most
+//          half of the step at its largest magnitude (1, then 1/2 of the next
+//          plane's unit), so the five stand for the value to within s / 4096
+//          <= amax / 12288.  A token is then five columns, which the tensor
+//          core has to spare.
 //
-// Per block (320 threads):
-//   warps 0..3  epilogue (thread = row);   warps 4..7  token side: operand
-//   rows and all scales by cp.async;       (both: phase 1, the selection and
-//   the conversion of h)   warp 8  weights by TMA;   warp 9  MMA issue.
+// Per block (352 threads):
+//   warps 0..7  phase 1, selection, image of h; warps 0..3 the epilogues
+//               (thread = row);
+//   warp 8      plans the jobs of the block's shares, and loads weights and
+//               their scales;
+//   warp 9      MMA issue;          warp 10  loads the tokens' images.
 // The weights stream past L2, so at every call the code itself comes from HBM:
 // a phase's first instructions cost as much as its first weights.  The role
 // loops therefore run both phases through the same code (measured: 172 KB of
@@ -58,17 +68,38 @@ namespace {
 
 constexpr int CW = 8;                          // general warps
 constexpr int CT = CW * 32;
-constexpr int W_TMA = 8, W_MMA = 9;
-constexpr int THREADS = CT + 64;
-constexpr int EPI = 128;                       // epilogue threads, and token-side threads
+constexpr int W_LOAD = 8, W_MMA = 9, W_TOKENS = 10;
+constexpr int THREADS = CT + 96;
+constexpr int EPI = 128;                       // epilogue threads
 constexpr int NP = 2;                          // pieces per slot
 constexpr int MAX_SLOTS = 5, PIECE_BYTES = 16384;
 constexpr int MAX_T = MOE_FEW_MAX_TOKENS;
-constexpr int MAX_BLOCKS = 256;
+constexpr int MAX_BLOCKS = 160;                // SMs used
+constexpr int SMALL = 8, SHARES = 1 + SMALL;   // shares of a phase per block, at most: one large, the others small
+constexpr int JOBS = 4, JOB_PIECES = 64;       // jobs announced within a block; pieces of a job
 constexpr int PLANES = 5;                      // MXFP4: columns per token
-constexpr uint32_t ACC_COLS = 96, SF_COL0 = 2 * ACC_COLS, SF_COLS = 32, TMEM_COLS = 256;
+constexpr int SLICE_PIECES = 14;               // router: a slice of d has at most 14 x 128 columns
+constexpr uint32_t ACC_COLS = 96, SFB_COL0 = 2 * ACC_COLS, SFB_COLS = 16, SFA_COL0 = SFB_COL0 + 2 * SFB_COLS;
+constexpr uint32_t TMEM_COLS = 256;            // 2 accumulators; 2 slots of token scales; weight scales (32 columns)
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
+
+// A job: a run of slots of one tile and one matrix: pieces p0 .. p1 - 1 of K
+// (128 bytes of every row each) of rows row0 .. row0 + 127, for the tokens of
+// `mask`.  Column c of the operand is token c / P (phase 2: of all; phase 3:
+// the c / P-th of mask).
+struct Job {
+    int shared;                  // 1: shared expert
+    int mat, row0;
+    int n, k;                    // the matrix: n rows of k columns
+    int p0, p1;                  // -1: the phase is over
+    uint32_t mask;
+    uint64_t kpack;              // routed: the tokens' slots, 4 bits each
+    int ends;                    // the share's last job of this tile
+    int share, share0, share1;   // this share, and the first and last with slots of the tile
+    int base8;                   // phase 3: first row of the expert's image, in units of 8
+    int rank;                    // phase 3: its place among the experts reached (shared: its number)
+};
 
 constexpr int OFF_IDX = 0;                                     // [16][16] int
 constexpr int OFF_GATE = OFF_IDX + MAX_T * 16 * 4;             // [16][16] float
@@ -76,18 +107,24 @@ constexpr int OFF_MASK = OFF_GATE + MAX_T * 16 * 4;            // [256] tokens k
 constexpr int OFF_KPACK = OFF_MASK + 256 * 4;                  // [256] 4 bits per token: its slot
 constexpr int OFF_ACT = OFF_KPACK + 256 * 8;                   // [256] experts reached, ascending
 constexpr int OFF_COUNT = OFF_ACT + 256 * 4;                   // [256] slots that name the expert
-constexpr int OFF_OUT = OFF_COUNT + 256 * 4;                   // [16][128] fp32 sums of a tile
-constexpr int OFF_BAR = OFF_OUT + MAX_T * 128 * 4;             // full, empty [MAX_SLOTS]; accf, acce [2]; drain
-constexpr int OFF_MISC = OFF_BAR + (2 * MAX_SLOTS + 5) * 8;    // abort flag, n_active, tmem address, last flag, 8 warp counts
-constexpr int OFF_RING = (OFF_MISC + 64 + 1023) & ~1023;
-constexpr int RING_BYTES = 206 * 1024;
+constexpr int OFF_BASE = OFF_COUNT + 256 * 4;                  // [256] per expert: base8 | rank << 16
+constexpr int OFF_OUT = OFF_BASE + 256 * 4;                    // [16][128] fp32 sums of a tile
+constexpr int OFF_UNI = OFF_OUT + MAX_T * 128 * 4;             // [512] a uniform set of weight scales, on its way
+constexpr int OFF_JOBS = OFF_UNI + 512;                        // [JOBS] Job
+constexpr int OFF_JOBSC = OFF_JOBS + JOBS * static_cast<int>(sizeof(Job));     // [JOBS][64] FP8: weight scales, UE8M0
+constexpr int OFF_BAR = OFF_JOBSC + JOBS * JOB_PIECES;         // full, empty [MAX_SLOTS]; accf, acce [2]; drain; jobs' full, empty
+constexpr int N_BARS = 2 * MAX_SLOTS + 5 + 2 * JOBS;
+constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;                 // abort flag, n_active, tmem address, last flag, 8 warp counts, 8 warp sums
+constexpr int OFF_RING = (OFF_MISC + 96 + 1023) & ~1023;
+constexpr int RING_BYTES = 207 * 1024;
 constexpr int SMEM_ALLOC = OFF_RING + RING_BYTES + 1024;
 static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
-static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
-static_assert(SF_COL0 + 2 * SF_COLS <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
+static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0 && OFF_JOBS % 8 == 0 && sizeof(Job) % 8 == 0 && OFF_UNI % 16 == 0,
+              "alignment");
+static_assert(SFA_COL0 + 32 <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
 
 // grid-wide counters in the workspace, zero between launches
-enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_WORDS = 5, CTR_TILE = 64 };
+enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_SHARE = 5, CTR_WORDS = 7, CTR_TILE = 64 };
 
 struct __align__(64) FewParams {
     CUtensorMap w1, w2, ws1, ws2;
@@ -104,16 +141,16 @@ struct __align__(64) FewParams {
     // workspace
     int32_t* status;
     uint32_t* ctr;
-    float* part;                  // (ks, T, E) partial logits
+    float* part;                  // (ks, T, E rounded up to 4) partial logits
     float* prob;                  // (T, 256) softmax of the logits
-    uint8_t* xq;                  // x in operand form (bf16: x itself)
-    uint8_t* xs;                  // its scales: FP8 a word per 128 columns, MXFP4 a byte per 32
+    uint8_t *xq, *xs;             // image of x: rows, scales
+    uint8_t *hq, *hs;             // image of h, routed
+    uint8_t *hqs, *hss;           // image of h, shared
     float* h32;                   // fp32 h: (T K, dff), then (S T, dffs)
-    uint8_t* hq;                  // h in operand form, same rows (bf16: the only form)
-    uint8_t* hs;                  // its scales
-    float* sums;                  // (blocks, 2, T, 128) parts of tiles that cross blocks
+    float* sums;                  // (shares, 2, T, 128) parts of tiles that cross shares
     float alpha;
     int T, d, E, K, dff, S, dffs, capacity, slot_major, passthrough;
+    int e4;                       // E rounded up to 4
     int ks, slice;                // router slices of d and their length
     int slots, slot_bytes;        // ring
 };
@@ -121,31 +158,36 @@ struct __align__(64) FewParams {
 enum { M_BF16 = 0, M_FP8 = 1, M_FP4 = 2 };
 
 // KP: elements of K in a piece (128 bytes of a weight row); P: columns per
-// token; SF: bytes of scales per piece (weights', then tokens')
+// token; SFB, SFA: bytes of the tokens' and the weights' scales per piece
 template <int MODE> struct Form;
-template <> struct Form<M_BF16> { static constexpr int KP = 64, P = 1, SF = 0; };
-template <> struct Form<M_FP8> { static constexpr int KP = 128, P = 1, SF = 1024; };
-template <> struct Form<M_FP4> { static constexpr int KP = 256, P = PLANES, SF = 2048; };
+template <> struct Form<M_BF16> { static constexpr int KP = 64, P = 1, SFB = 0, SFA = 0; };
+template <> struct Form<M_FP8> { static constexpr int KP = 128, P = 1, SFB = 512, SFA = 0; };
+template <> struct Form<M_FP4> { static constexpr int KP = 256, P = PLANES, SFB = 1024, SFA = 1024; };
 
 __host__ __device__ constexpr int round16(int v) { return (v + 15) & ~15; }
+// Rows of an image for n tokens, in units of 8 (1024 bytes a piece).
+template <int MODE> __host__ __device__ constexpr int rows8(int n) { return (n * Form<MODE>::P + 7) / 8; }
+// Pieces of k columns, counted in whole slots.
+template <int MODE> __host__ __device__ constexpr int slots_of(int k) { return (k + NP * Form<MODE>::KP - 1) / (NP * Form<MODE>::KP); }
+template <int MODE> __host__ __device__ constexpr int pieces_of(int k) { return NP * slots_of<MODE>(k); }
 
 __device__ __forceinline__ void bar_general() { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); }
-
-__device__ __forceinline__ void bar_tokens() { asm volatile("bar.sync 3, %0;" :: "n"(EPI) : "memory"); }
 __device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 2, %0;" :: "n"(EPI) : "memory"); }
+__device__ __forceinline__ void bar_upper() { asm volatile("bar.sync 3, %0;" :: "n"(EPI) : "memory"); }       // warps 4..7
+// The general warps and the token loader: what phase 2 or 3 reads is in memory.
+__device__ __forceinline__ void bar_tokens_ready() { asm volatile("bar.sync 4, %0;" :: "n"(CT + 32) : "memory"); }
 
-__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+// Orders generic-proxy writes of global memory with async-proxy (bulk copy)
+// reads of it: by the writer before the barrier, by the reader after it.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-// Arrives on bar once this thread's earlier cp.async copies have landed (the
-// barrier's count includes the arrival).
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
@@ -154,14 +196,30 @@ __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     return v;
 }
 
-// ---------------------------------------------------------------- operand form of x and h
+// ---------------------------------------------------------------- images of x and h
+//
+// Rows: per piece, the columns' rows of 128 bytes, as many groups of 8 as the
+// tokens need, 16-byte chunk q of row n at chunk q ^ (n mod 8) (the 128-byte
+// swizzle).  Scales: per 128 columns of K, 512 bytes with column n's word (the
+// UE8M0 bytes of its four blocks of 32) at 16 (n mod 32) + 4 (n div 32).
 
-// 128 consecutive values of row `row` (a token of x, a slot of h) starting at
-// column col, four per lane, into the operand form of rows of k columns.
+// Four consecutive values a lane, 128 in all, of column block `col` (a
+// multiple of 128), for the c-th token of an image whose pieces have r8 groups
+// of rows.
 template <int MODE>
-__device__ __noinline__ void store_block(float4 v4, uint8_t* q, uint8_t* scales, size_t row, int k, int col, int lane) {
+__device__ __noinline__ void store_block(float4 v4, uint8_t* rows, uint8_t* scales, int r8, int c, int col, int lane) {
     float v[4] = {v4.x, v4.y, v4.z, v4.w};
-    if (MODE == M_FP8) {
+    // byte `at` of row n of the piece that has it
+    auto place = [&](int n, int at) {
+        return rows + (static_cast<size_t>(at >> 7) * r8 + (n >> 3)) * 1024 + (n & 7) * 128 +
+               ((((at >> 4) & 7) ^ (n & 7)) << 4) + (at & 15);
+    };
+    auto word = [&](int n) { return scales + static_cast<size_t>(col / 128) * 512 + 16 * (n & 31) + 4 * (n >> 5); };
+    if (MODE == M_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(place(c, 2 * (col + 4 * lane))) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else if (MODE == M_FP8) {
         // as the dispatch quantiser: fmaxf does not count a NaN
         float a = 0.f;
 #pragma unroll
@@ -169,10 +227,8 @@ __device__ __noinline__ void store_block(float4 v4, uint8_t* q, uint8_t* scales,
         const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
         const float sc = pow2_scale_448(__uint_as_float(m)), inv = inv_pow2(sc);
         const uint32_t lo = f32x2_to_e4m3x2(v[0] * inv, v[1] * inv), hi = f32x2_to_e4m3x2(v[2] * inv, v[3] * inv);
-        reinterpret_cast<uint32_t*>(q + row * k + col)[lane] = lo | (hi << 16);
-        // the scale's UE8M0 byte, once per 32 columns
-        if (lane == 0) reinterpret_cast<uint32_t*>(scales)[row * (k / 128) + col / 128] =
-            (__float_as_uint(sc) >> 23) * 0x01010101u;
+        *reinterpret_cast<uint32_t*>(place(c, col + 4 * lane)) = lo | (hi << 16);
+        if (lane == 0) *reinterpret_cast<uint32_t*>(word(c)) = (__float_as_uint(sc) >> 23) * 0x01010101u;
     } else {
         // eight lanes have a block of 32
         uint32_t m = 0;
@@ -194,10 +250,9 @@ __device__ __noinline__ void store_block(float4 v4, uint8_t* q, uint8_t* scales,
             e2m1x4_to_f32(codes, back);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = (v[j] - back[j]) * (pl == 0 ? 4.f : 8.f);
-            const size_t r = row * PLANES + pl;
-            reinterpret_cast<uint16_t*>(q + (r * k + col) / 2)[lane] = static_cast<uint16_t>(codes);
-            if ((lane & 7) == 0)
-                scales[(r * k + col) / 32 + lane / 8] = static_cast<uint8_t>(b == 255u ? 255 : max(e, 0));
+            const int n = c * PLANES + pl;
+            *reinterpret_cast<uint16_t*>(place(n, col / 2 + 2 * lane)) = static_cast<uint16_t>(codes);
+            if ((lane & 7) == 0) word(n)[lane / 8] = static_cast<uint8_t>(b == 255u ? 255 : max(e, 0));
         }
     }
 }
@@ -218,6 +273,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Ctx& 
     return mbar_wait_bounded(bar, parity, c.abort_flag, c.p.status, kWaitNs);
 }
 
+// wait() for a whole warp, which stays converged.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Ctx& c) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait(bar, parity, c));
+}
+
 // The general warps of all blocks.  Writes before it are visible to reads
 // (through L2) after it.
 __device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* status, volatile int* abort_flag, int tid) {
@@ -228,6 +289,7 @@ __device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* st
         atomicAdd(ctr, 1u);
         if (*abort_flag) atomicExch(ctrs + CTR_ABORT, 1u);
         uint64_t t0 = 0;
+#pragma unroll 1
         for (uint32_t it = 1; !*abort_flag && ld_acquire(ctr) < gridDim.x; ++it) {
             if ((it & 255u) == 0) {
                 const uint64_t now = global_timer_ns();
@@ -247,75 +309,75 @@ __device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* st
 
 // ---------------------------------------------------------------- jobs
 
-// A job: a run of slots of one tile and one matrix: pieces p0 .. p1 - 1 of K
-// (128 bytes of every row each) of rows row0 .. row0 + 127, for the tokens of
-// `mask`; the j-th of them has the columns j P .. j P + P - 1.
-struct Job {
-    int shared;           // 1: shared expert
-    int mat, row0;
-    int n, k;             // the matrix: n rows of k columns
-    int p0, p1;
-    uint32_t mask;
-    uint64_t kpack;       // routed: the tokens' slots
-    bool ends;            // the block's last job of this tile
-    // the blocks that have slots of this tile
-    int block0, block1;
-};
-
-// Row of h for token t of a job.
+// Row of h32 for token t of a job.
 __device__ __forceinline__ int h_row(const Ctx& c, const Job& j, int t) {
     return j.shared ? j.mat * c.p.T + t : t * c.p.K + (static_cast<int>(j.kpack >> (4 * t)) & 15);
 }
 
-// This block's share of a phase's slots, job by job.  Phase 2: matrix by
-// matrix, its tiles, their slots of K = d.  Phase 3: tile by tile, the shared
-// experts' slots, then those of the experts reached.
+// Place of token t among the columns of its expert's image of h.
+__device__ __forceinline__ int column_of(const Job& j, int t) { return __popc(j.mask & ((1u << t) - 1u)); }
+
+// The shares of a phase's slots and their jobs (planning warp).  Phase 2:
+// matrix by matrix, its tiles, their slots of K = d.  Phase 3: tile by tile,
+// the shared experts' slots, then those of the experts reached.
 template <int MODE>
-struct Jobs {
+struct Plan {
     const Ctx& c;
-    const bool third;     // phase 3
-    int at, end;
-    int each, extra;      // slots of a block; the first `extra` blocks have one more
+    bool third;           // phase 3
+    int share, shares, at, end;
+    int lead;             // slots of the large shares, one per block (0: none)
+    int each, extra;      // slots of the others; the first `extra` have one more
     int ss, sr;           // slots of a shared, a routed matrix per tile
     int ts, tr;           // phase 2: tiles of a shared, a routed matrix
     int tile;             // phase 3: slots of a tile
-    static __device__ __forceinline__ int slots_of(int k) { return (k + NP * Form<MODE>::KP - 1) / (NP * Form<MODE>::KP); }
-    __device__ __forceinline__ Jobs(const Ctx& c_, int phase, int n_active) : c(c_), third(phase == 3) {
+    __device__ __forceinline__ Plan(const Ctx& c_, int phase, int n_active) : c(c_), third(phase == 3) {
         const FewParams& p = c.p;
-        int all;
-        if (!third) {
-            ss = sr = slots_of(p.d);
-            ts = (p.dffs + 127) / 128;
-            tr = (p.dff + 127) / 128;
-            tile = 1;
-            all = (p.S * ts + n_active * tr) * sr;
+        ss = slots_of<MODE>(third ? p.dffs : p.d);
+        sr = slots_of<MODE>(third ? p.dff : p.d);
+        ts = third ? 1 : (p.dffs + 127) / 128;
+        tr = third ? 1 : (p.dff + 127) / 128;
+        tile = third ? p.S * ss + n_active * sr : 1;
+        const int all = third ? (p.d + 127) / 128 * tile : (p.S * ts + n_active * tr) * sr;
+        // Fewer than 64 slots a block: equal shares (none without slots; the
+        // join of a further share costs more than it evens out).  Else three
+        // quarters in large shares and the rest in small ones of 12 slots or more.
+        const int blocks = gridDim.x, per = all / blocks;
+        lead = per < 64 ? 0 : 3 * per / 4;
+        const int others = lead ? blocks * max(1, min(SMALL, (per - lead) / 12)) : min(blocks, all);
+        shares = others + (lead ? blocks : 0);
+        each = (all - blocks * lead) / others;
+        extra = all - blocks * lead - each * others;
+        at = end = 0;
+    }
+    __device__ __forceinline__ void take(int s) {
+        share = s;
+        const int blocks = gridDim.x;
+        if (lead && s < blocks) {
+            at = s * lead;
+            end = at + lead;
         } else {
-            ss = slots_of(p.dffs);
-            sr = slots_of(p.dff);
-            ts = tr = 1;
-            tile = p.S * ss + n_active * sr;
-            all = (p.d + 127) / 128 * tile;
+            const int v = lead ? s - blocks : s;
+            at = blocks * lead + v * each + min(v, extra);
+            end = at + each + (v < extra ? 1 : 0);
         }
-        // with fewer slots than blocks the last blocks have none, so that every
-        // block between a tile's first and last has some of it
-        const int b = blockIdx.x;
-        each = all / static_cast<int>(gridDim.x);
-        extra = all - each * static_cast<int>(gridDim.x);
-        at = b * each + min(b, extra);
-        end = at + each + (b < extra ? 1 : 0);
     }
-    // the block that has slot u
-    __device__ __forceinline__ int block_of(int u) const {
+    // the share that has slot u
+    __device__ __forceinline__ int share_of(int u) const {
+        const int blocks = gridDim.x;
+        if (u < blocks * lead) return u / lead;
+        u -= blocks * lead;
         const int v = u - extra * (each + 1);
-        return v < 0 ? u / (each + 1) : extra + v / each;
+        return (lead ? blocks : 0) + (v < 0 ? u / (each + 1) : extra + v / each);
     }
+    // The share's next job; false at its end.
     __device__ __forceinline__ bool next(Job& j) {
         if (at >= end) return false;
         const FewParams& p = c.p;
         int u = at, first = 0;
         if (third) {
-            j.row0 = u / tile * 128;
-            first = u / tile * tile;
+            const int t = u / tile;
+            j.row0 = t * 128;
+            first = t * tile;
             u -= first;
         }
         const int n_shared = p.S * ts * ss;
@@ -328,21 +390,53 @@ struct Jobs {
             j.row0 = (run - m * tiles) * 128;
             first = at - s0;
         }
-        const int take = min(per - s0, end - at);
+        const int n = min(min(per - s0, end - at), JOB_PIECES / NP);
         j.mat = j.shared ? m : reinterpret_cast<const int*>(c.smem + OFF_ACT)[m];
         j.mask = j.shared ? (1u << p.T) - 1u : reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK)[j.mat];
         j.kpack = j.shared ? 0 : reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK)[j.mat];
+        const int base = j.shared ? 0 : reinterpret_cast<const int*>(c.smem + OFF_BASE)[j.mat];
+        j.base8 = j.shared ? m * rows8<MODE>(p.T) : base & 0xFFFF;
+        j.rank = j.shared ? m : base >> 16;
         const int inner = j.shared ? p.dffs : p.dff;
         j.n = third ? p.d : inner;
         j.k = third ? inner : p.d;
         j.p0 = s0 * NP;
-        j.p1 = min((s0 + take) * NP, (j.k + Form<MODE>::KP - 1) / Form<MODE>::KP);
-        at += take;
+        j.p1 = min((s0 + n) * NP, (j.k + Form<MODE>::KP - 1) / Form<MODE>::KP);
+        at += n;
         const int last = first + (third ? tile : per) - 1;
         j.ends = at == end || at > last;
-        j.block0 = block_of(first);
-        j.block1 = block_of(last);
+        j.share = share;
+        j.share0 = share_of(first);
+        j.share1 = share_of(last);
         return true;
+    }
+};
+
+// The jobs of the block, in order, from the planning warp to every other role;
+// p0 = -1 ends a phase.
+constexpr uint32_t JOB_READERS = 4 + 2;       // epilogue warps, MMA, token loader
+struct JobQueue {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step() { if (++at == JOBS) { at = 0; phase ^= 1u; } }
+    __device__ __forceinline__ static uint64_t* full(const Ctx& c, int i) { return c.full + 2 * MAX_SLOTS + 5 + i; }
+    __device__ __forceinline__ static uint64_t* empty(const Ctx& c, int i) { return full(c, JOBS + i); }
+    __device__ __forceinline__ static Job* job(const Ctx& c, int i) { return reinterpret_cast<Job*>(c.smem + OFF_JOBS) + i; }
+    // A whole warp: its copy of the next job; false at the end of a phase, and
+    // after a wait gave up (ok becomes false).
+    __device__ __forceinline__ bool next(const Ctx& c, Job& j, bool& ok) {
+        if (ok) ok = wait_warp(full(c, at), phase, c);
+        if (!ok) return false;
+        j = *job(c, at);
+        const bool more = j.p0 >= 0;
+        if (!more) done(c);
+        return more;
+    }
+    // after the last use of the queue's copy of the job (or of its scales)
+    __device__ __forceinline__ void done(const Ctx& c) {
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive(empty(c, at));
+        step();
     }
 };
 
@@ -352,138 +446,95 @@ struct Ring {
     __device__ __forceinline__ void next(int slots) { if (++slot == slots) { slot = 0; phase ^= 1u; } }
 };
 
-// A slot of the ring: NP pieces of weights, the tokens' rows of each, the
-// scales of each.
+// A slot of the ring: NP pieces of weights; the tokens' rows of each, r8
+// groups of 8; their scales; MXFP4: the weights' scales.
 __device__ __forceinline__ uint8_t* slot_at(const Ctx& c, int slot) { return c.smem + OFF_RING + slot * c.p.slot_bytes; }
-template <int MODE>
-__device__ __forceinline__ int rows_bytes(const Ctx& c) { return round16(c.p.T * Form<MODE>::P) * 128; }
-template <int MODE>
-__device__ __forceinline__ int scales_at(const Ctx& c) { return NP * (PIECE_BYTES + rows_bytes<MODE>(c)); }
+template <int MODE> __host__ __device__ constexpr int sfb_at(int T) { return NP * (PIECE_BYTES + 1024 * rows8<MODE>(T)); }
+template <int MODE> __host__ __device__ constexpr int sfa_at(int T) { return sfb_at<MODE>(T) + NP * Form<MODE>::SFB; }
 
-// ---------------------------------------------------------------- weights (one warp)
+// ---------------------------------------------------------------- planning and weights (one warp)
 
-// Loads a job's weights; false after a wait gave up.
+// Announces a job; FP8: with the UE8M0 bytes of its pieces' weight scales.
 template <int MODE>
-__device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const CUtensorMap* map, Ring& ring) {
+__device__ __forceinline__ bool post(const Ctx& c, JobQueue& q, const Job& j, const float* scales) {
+    uint32_t s[JOB_PIECES / 32] = {};
+    if (MODE == M_FP8 && j.p0 >= 0) {
+        const float* row = scales + (static_cast<size_t>(j.mat) * (j.n / 128) + j.row0 / 128) * (j.k / 128) + j.p0;
+#pragma unroll
+        for (int i = 0; i < JOB_PIECES / 32; ++i)
+            if (32 * i + c.lane < j.p1 - j.p0) s[i] = (__float_as_uint(__ldg(row + 32 * i + c.lane)) >> 23) & 0xFFu;
+    }
+    if (!wait_warp(JobQueue::empty(c, q.at), q.phase ^ 1u, c)) return false;
+    if (MODE == M_FP8) {
+#pragma unroll
+        for (int i = 0; i < JOB_PIECES / 32; ++i)
+            c.smem[OFF_JOBSC + q.at * JOB_PIECES + 32 * i + c.lane] = static_cast<uint8_t>(s[i]);
+    }
+    if (c.lane == 0) *JobQueue::job(c, q.at) = j;
+    __syncwarp();
+    if (c.lane == 0) mbar_arrive(JobQueue::full(c, q.at));
+    q.step();
+    return true;
+}
+
+// Loads a job's weights, and their MXFP4 scales: 512 bytes per 128 rows and
+// 128 columns, tile by tile.
+template <int MODE>
+__device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const CUtensorMap* map, const uint8_t* scales,
+                                             Ring& ring) {
     constexpr int ELEMS = MODE == M_BF16 ? 64 : 128;        // map elements (bf16, or bytes) per piece
+    const int words = j.k / 128;
+    const uint8_t* sc = scales + (static_cast<size_t>(j.mat) * ((j.n + 127) / 128) + j.row0 / 128) * words * 512;
+#pragma unroll 1
     for (int s = j.p0; s < j.p1; s += NP) {
+        if (!wait_warp(c.empty + ring.slot, ring.phase ^ 1u, c)) return false;
         uint64_t* full = c.full + ring.slot;
+        uint8_t* slot = slot_at(c, ring.slot);
         const int np = min(NP, j.p1 - s);
-        int ok = 1;
+        const uint32_t sfa = MODE == M_FP4 ? 512u * min(2 * NP, words - 2 * s) : 0u;
         if (c.lane == 0) {
-            ok = wait(c.empty + ring.slot, ring.phase ^ 1u, c);
-            if (ok) mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * PIECE_BYTES));
+            mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * PIECE_BYTES) + sfa);
+            tma_load_3d(slot, map, full, s * ELEMS, j.row0, j.mat);
+            if (np > 1) tma_load_3d(slot + PIECE_BYTES, map, full, (s + 1) * ELEMS, j.row0, j.mat);
+            if (MODE == M_FP4) bulk_load(slot + sfa_at<MODE>(c.p.T), sc + static_cast<size_t>(s) * 1024, sfa, full);
         }
-        if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-        if (c.lane < np)
-            tma_load_3d(slot_at(c, ring.slot) + c.lane * PIECE_BYTES, map, full, (s + c.lane) * ELEMS, j.row0, j.mat);
+        __syncwarp();
         ring.next(c.p.slots);
     }
     return true;
 }
 
-// ---------------------------------------------------------------- token side (128 threads)
+// ---------------------------------------------------------------- tokens (one warp)
 
-// The tokens' operand rows and the scales of every piece of a phase's jobs,
-// copied by cp.async; the copies' own completion arrives on the slot's barrier.
-// (The tensor core reads them through the async proxy: the MMA thread, which
-// has nothing else in flight, makes the proxy fence.  Made here it would wait
-// for the copies just issued: measured 1000 cycles a piece.)
+// Loads the tokens' rows and scales of a job's slots.
 template <int MODE>
-__device__ __forceinline__ void load_tokens(const Ctx& c, int phase, int n_active, size_t h_shared, Ring& ring, bool& ok) {
-    constexpr int P = Form<MODE>::P, KP = Form<MODE>::KP;
+__device__ __forceinline__ bool load_tokens(const Ctx& c, const Job& j, bool third, Ring& ring) {
     const FewParams& p = c.p;
-    const bool third = phase == 3;
-    const int i = c.tid - EPI;
-    const int q = i & 7;                                       // 16-byte chunk of a row's 128 bytes
-    const int word = 16 * (i & 31) + 4 * (i >> 5);             // row i's word in 512 bytes of scales
-    const int row_bytes = rows_bytes<MODE>(c), sf_at = scales_at<MODE>(c);
-    Jobs<MODE> jobs(c, phase, n_active);
-    Job j;
-    while (ok && jobs.next(j)) {
-        const int rows = __popc(j.mask) * P;
-        // bytes of an operand row of j.k columns
-        const size_t pitch = MODE == M_BF16 ? 2 * static_cast<size_t>(j.k) : MODE == M_FP8 ? j.k : j.k / 2;
-        const int kq = MODE == M_FP8 ? j.k / 128 * 4 : j.k / 32;   // and of its scales
-        // shared experts' rows of h follow the routed ones, at their own width
-        const uint8_t* data = third ? p.hq : p.xq;
-        const uint8_t* sc = third ? p.hs : p.xs;
-        if (third && j.shared) {
-            const size_t skip = h_shared * P;
-            data += MODE == M_BF16 ? 2 * skip : MODE == M_FP8 ? skip : skip / 2;
-            sc += MODE == M_FP8 ? skip / 128 * 4 : skip / 32;
-        }
-        auto operand_row = [&](int n) {                        // of column n
-            uint32_t m = j.mask;
-            for (int z = n / P; z > 0; --z) m &= m - 1;
-            const int t = __ffs(m) - 1;
-            return static_cast<size_t>((third ? h_row(c, j, t) : t) * P + n % P);
-        };
-        const uint8_t* src[P];                                 // 16 rows at a time, 16 P in all
-#pragma unroll
-        for (int b = 0; b < P; ++b) {
-            const int n = (i >> 3) + 16 * b;
-            src[b] = n < rows ? data + operand_row(n) * pitch + 16 * q : nullptr;
-        }
-        const uint8_t* bs = nullptr;                           // scales of column i
-        const uint8_t* as = nullptr;                           // scales of weight row i
-        if (MODE != M_BF16) {
-            if (i < rows) bs = sc + operand_row(i) * kq;
-            if (j.row0 + i < j.n) {
-                const uint8_t* w = static_cast<const uint8_t*>(third ? (j.shared ? p.ws2s : p.w2s) : (j.shared ? p.ws1s : p.w1s));
-                as = MODE == M_FP8 ? w + (static_cast<size_t>(j.mat) * (j.n / 128) + j.row0 / 128) * kq
-                                   : w + (static_cast<size_t>(j.mat) * j.n + j.row0 + i) * kq;
-            }
-        }
-        float wsc[NP];                                         // FP8: the tile's weight scales, a slot ahead
-        auto fetch = [&](int s) {
-#pragma unroll
-            for (int r = 0; r < NP; ++r)
-                wsc[r] = s + r < j.p1 ? __ldg(reinterpret_cast<const float*>(as) + s + r) : 0.f;
-        };
-        if (MODE == M_FP8) fetch(j.p0);
-        for (int s = j.p0; s < j.p1; s += NP) {
-            int w = 1;
-            if (c.lane == 0) w = wait(c.empty + ring.slot, ring.phase ^ 1u, c);
-            if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
-            uint8_t* slot = slot_at(c, ring.slot);
-#pragma unroll
-            for (int r = 0; r < NP; ++r) {
-                const int piece = s + r;
-                if (piece >= j.p1) break;
-                uint8_t* bdst = slot + NP * PIECE_BYTES + r * row_bytes;
-#pragma unroll
-                for (int b = 0; b < P; ++b) {
-                    const int n = (i >> 3) + 16 * b;
-                    if (src[b] && (MODE != M_FP4 || static_cast<size_t>(piece) * 128 + 16 * q < pitch))
-                        cp_async_16(bdst + n * 128 + ((q ^ (n & 7)) << 4), src[b] + static_cast<size_t>(piece) * 128);
-                }
-                uint8_t* sf = slot + sf_at + r * Form<MODE>::SF + word;
-                if (MODE == M_FP8) {
-                    // the weight scale's UE8M0 byte, once per 32 columns
-                    *reinterpret_cast<uint32_t*>(sf) = ((__float_as_uint(wsc[r]) >> 23) & 0xFFu) * 0x01010101u;
-                    if (bs) cp_async_4(sf + 512, bs + 4 * piece);
-                }
-                if (MODE == M_FP4) {
-                    const bool two = piece * KP + 128 < j.k;   // the piece's second 128 columns exist
-                    if (as) {
-                        cp_async_4(sf, as + 8 * piece);
-                        if (two) cp_async_4(sf + 512, as + 8 * piece + 4);
-                    }
-                    if (bs) {
-                        cp_async_4(sf + 1024, bs + 8 * piece);
-                        if (two) cp_async_4(sf + 1536, bs + 8 * piece + 4);
-                    }
-                }
-            }
-            cp_async_arrive(c.full + ring.slot);
-            if (MODE == M_FP8) {
-                mbar_arrive(c.full + ring.slot);               // the scales stored above
-                fetch(s + NP);
-            }
-            ring.next(c.p.slots);
-        }
+    const int r8 = rows8<MODE>(third ? __popc(j.mask) : p.T);
+    const int pieces = pieces_of<MODE>(j.k);
+    const uint8_t* rows = p.xq;
+    const uint8_t* scales = p.xs;
+    if (third) {
+        rows = (j.shared ? p.hqs : p.hq) + static_cast<size_t>(j.base8) * pieces * 1024;
+        scales = (j.shared ? p.hss : p.hs) + static_cast<size_t>(j.rank) * pieces * Form<MODE>::SFB;
     }
+    // (a slot's second piece may lie past K: the image has it, of any contents)
+    const uint32_t bytes = NP * 1024u * r8;
+#pragma unroll 1
+    for (int s = j.p0; s < j.p1; s += NP) {
+        if (!wait_warp(c.empty + ring.slot, ring.phase ^ 1u, c)) return false;
+        if (c.lane == 0) {
+            uint64_t* full = c.full + ring.slot;
+            uint8_t* slot = slot_at(c, ring.slot);
+            mbar_arrive_expect_tx(full, bytes + NP * Form<MODE>::SFB);
+            bulk_load(slot + NP * PIECE_BYTES, rows + static_cast<size_t>(s) * r8 * 1024, bytes, full);
+            if (MODE != M_BF16)
+                bulk_load(slot + sfb_at<MODE>(p.T), scales + static_cast<size_t>(s) * Form<MODE>::SFB, NP * Form<MODE>::SFB, full);
+        }
+        __syncwarp();
+        ring.next(p.slots);
+    }
+    return true;
 }
 
 // ---------------------------------------------------------------- MMA issue (one warp)
@@ -494,8 +545,9 @@ __device__ __forceinline__ void load_tokens(const Ctx& c, int phase, int n_activ
 
 struct MmaState {
     Ring ring;
-    int jobs = 0, slots = 0;
+    int jobs = 0, slots = 0, rewrites = 0;
     bool leader;
+    uint32_t tags = 0x100u;      // FP8, lane i: the exponent whose uniform scales are in set i
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -504,30 +556,52 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// wait() for a whole warp, which stays converged.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Ctx& c) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, wait(bar, parity, c));
+// FP8: the columns with the weight scale 2^(e - 127) for every row.  A set is
+// rewritten when another exponent of the same residue comes up, once the MMAs
+// issued before, which may read it, are done.
+__device__ __forceinline__ bool uniform_scales(const Ctx& c, MmaState& st, uint32_t tmem, uint32_t e, uint32_t& cols) {
+    const uint32_t set = e & 7u;
+    cols = tmem + SFA_COL0 + 4 * set;
+    if (__shfl_sync(0xffffffffu, st.tags, static_cast<int>(set)) == e) return true;
+    uint64_t* bar = c.full + 2 * MAX_SLOTS + 4;             // the drain barrier
+#pragma unroll 1
+    for (int step = 0; step < 2; ++step) {                  // the MMAs before; the copy, whose source is then free
+        if (step == 1) {
+            const uint32_t w = e * 0x01010101u;
+            reinterpret_cast<uint4*>(c.smem + OFF_UNI)[c.lane] = make_uint4(w, w, w, w);
+            fence_proxy_async_smem();
+            __syncwarp();
+            tc_fence_after();
+            if (st.leader) tmem_cp_scales(cols, c.smem + OFF_UNI);
+        }
+        if (st.leader) umma_commit(bar);
+        __syncwarp();
+        if (!wait_warp(bar, static_cast<uint32_t>(st.rewrites & 1), c)) return false;
+        ++st.rewrites;
+    }
+    if (c.lane == static_cast<int>(set)) st.tags = e;
+    return true;
 }
 
 template <int MODE>
-__device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, uint32_t tmem, uint64_t* accf, uint64_t* acce,
-                                          MmaState& st) {
+__device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, const uint8_t* wscales, bool third, uint32_t tmem,
+                                          uint64_t* accf, uint64_t* acce, MmaState& st) {
     const int buf = st.jobs & 1;
     if (!wait_warp(acce + buf, ((st.jobs >> 1) & 1) ^ 1u, c)) return false;
     tc_fence_after();
     const uint32_t d = tmem + buf * ACC_COLS;
-    const uint32_t n = round16(__popc(__shfl_sync(0xffffffffu, j.mask, 0)) * Form<MODE>::P);
+    const int tokens = third ? __popc(__shfl_sync(0xffffffffu, j.mask, 0)) : c.p.T;
+    const uint32_t n = round16(tokens * Form<MODE>::P);
+    const uint32_t row_bytes = 1024u * rows8<MODE>(tokens);
     const uint32_t idesc = MODE == M_BF16 ? make_idesc(1, 128, n) : MODE == M_FP8 ? make_idesc_mxf8(128, n)
                                                                                  : make_idesc_mxf4(n, 0);
     const uint32_t idesc2 = MODE == M_FP4 ? make_idesc_mxf4(n, 2) : idesc;
     const int p0 = __shfl_sync(0xffffffffu, j.p0, 0), p1 = __shfl_sync(0xffffffffu, j.p1, 0);
     // MXFP4: the last piece of K may be a half
     const int whole = MODE == M_FP4 ? __shfl_sync(0xffffffffu, j.k, 0) / Form<MODE>::KP : p1;
-    const int row_bytes = rows_bytes<MODE>(c), sf_at = scales_at<MODE>(c);
+#pragma unroll 1
     for (int s = p0; s < p1; s += NP) {
         if (!wait_warp(c.full + st.ring.slot, st.ring.phase, c)) return false;
-        fence_proxy_async_smem();                              // the token side was copied through the generic proxy
         if (MODE != M_BF16 && st.slots >= 2) {
             // the MMAs that read this half of the scale columns two slots ago are done
             int q = st.ring.slot - 2;
@@ -535,145 +609,155 @@ __device__ __forceinline__ bool issue_job(const Ctx& c, const Job& j, uint32_t t
             if (q < 0) { q += c.p.slots; ph ^= 1u; }
             if (!wait_warp(c.empty + q, ph, c)) return false;
         }
-        tc_fence_after();
         uint8_t* slot = slot_at(c, st.ring.slot);
-        const uint32_t sf0 = tmem + SF_COL0 + (st.slots & 1) * SF_COLS;
+        tc_fence_after();
+        const uint32_t sfb0 = tmem + SFB_COL0 + (st.slots & 1) * SFB_COLS;
+        const uint32_t sfa0 = tmem + SFA_COL0 + (st.slots & 1) * SFB_COLS;
 #pragma unroll
         for (int r = 0; r < NP; ++r) {
             if (s + r >= p1) break;
+            uint32_t sfa = sfa0 + r * (SFB_COLS / NP);
+            if (MODE == M_FP8 && !uniform_scales(c, st, tmem, wscales[s + r - p0], sfa)) return false;
             const uint64_t a = smem_desc_k_sw128(slot + r * PIECE_BYTES);
             const uint64_t b = smem_desc_k_sw128(slot + NP * PIECE_BYTES + r * row_bytes);
             const uint32_t more = s + r > p0 ? 1u : 0u;
-            const uint8_t* sf = slot + sf_at + r * Form<MODE>::SF;
-            const uint32_t t = sf0 + r * (SF_COLS / NP);
+            const uint8_t* sfb_s = slot + sfb_at<MODE>(c.p.T) + r * Form<MODE>::SFB;
+            const uint8_t* sfa_s = slot + sfa_at<MODE>(c.p.T) + r * Form<MODE>::SFA;
+            const uint32_t sfb = sfb0 + r * (SFB_COLS / NP);
+            if (!st.leader) continue;
             if (MODE == M_BF16) {
-                if (st.leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, idesc, more | (k > 0));
-                }
+                for (int k = 0; k < 4; ++k) umma_f16(d, a + 2 * k, b + 2 * k, idesc, more | (k > 0));
             } else if (MODE == M_FP8) {
-                if (st.leader) {
-                    tmem_cp_scales(t, sf);
-                    tmem_cp_scales(t + 4, sf + 512);
+                tmem_cp_scales(sfb, sfb_s);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_mxf8_bs(d, a + 2 * k, b + 2 * k, idesc, t, t + 4, more | (k > 0));
-                }
+                for (int k = 0; k < 4; ++k) umma_mxf8_bs(d, a + 2 * k, b + 2 * k, idesc, sfa, sfb, more | (k > 0));
             } else {
-                if (st.leader) {
-                    tmem_cp_scales(t, sf);
-                    tmem_cp_scales(t + 8, sf + 1024);
-                    umma_mxf4_bs(d, a, b, idesc, t, t + 8, more);
-                    umma_mxf4_bs(d, a + 2, b + 2, idesc2, t, t + 8, 1);
-                    if (s + r < whole) {
-                        tmem_cp_scales(t + 4, sf + 512);
-                        tmem_cp_scales(t + 12, sf + 1536);
-                        umma_mxf4_bs(d, a + 4, b + 4, idesc, t + 4, t + 12, 1);
-                        umma_mxf4_bs(d, a + 6, b + 6, idesc2, t + 4, t + 12, 1);
-                    }
+                tmem_cp_scales(sfa, sfa_s);
+                tmem_cp_scales(sfb, sfb_s);
+                umma_mxf4_bs(d, a, b, idesc, sfa, sfb, more);
+                umma_mxf4_bs(d, a + 2, b + 2, idesc2, sfa, sfb, 1);
+                if (s + r < whole) {
+                    tmem_cp_scales(sfa + 4, sfa_s + 512);
+                    tmem_cp_scales(sfb + 4, sfb_s + 512);
+                    umma_mxf4_bs(d, a + 4, b + 4, idesc, sfa + 4, sfb + 4, 1);
+                    umma_mxf4_bs(d, a + 6, b + 6, idesc2, sfa + 4, sfb + 4, 1);
                 }
             }
         }
+        __syncwarp();
         ++st.slots;
         if (st.leader) umma_commit(c.empty + st.ring.slot);
         st.ring.next(c.p.slots);
     }
     if (st.leader) umma_commit(accf + buf);
+    __syncwarp();
     ++st.jobs;
     return true;
 }
 
 // ---------------------------------------------------------------- epilogue (128 threads, thread = row)
 
-// Waits for a job's accumulator and gives body(token, value) for every token
-// of the job, in ascending order.
-template <int MODE, typename F>
-__device__ __forceinline__ void read_job(const Ctx& c, const Job& j, uint32_t tmem, uint64_t* accf, uint64_t* acce,
-                                         int& jobs, bool& ok, F&& body) {
+// Adds a job's products to the thread's sums: out[t * 128] += gate * (v + bias).
+template <int MODE>
+__device__ __forceinline__ void read_job(const Ctx& c, const Job& j, bool third, float bias, uint32_t tmem, uint64_t* accf,
+                                         uint64_t* acce, int& jobs, bool& ok, float* out) {
     const int buf = jobs & 1;
-    if (ok) {
-        int w = 1;
-        if (c.lane == 0) w = wait(accf + buf, (jobs >> 1) & 1, c);
-        ok = __shfl_sync(0xffffffffu, w, 0) != 0;
-    }
+    if (ok) ok = wait_warp(accf + buf, (jobs >> 1) & 1, c);
     ++jobs;
     if (!ok) return;
     tc_fence_after();
     const uint32_t acc = tmem + (static_cast<uint32_t>(c.warp * 32) << 16) + buf * ACC_COLS;
-    uint32_t m = j.mask;
+    const bool gated = third && !j.shared;
+    auto add = [&](int t, float v) {
+        const float g = gated ? reinterpret_cast<const float*>(c.smem + OFF_GATE)[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)]
+                              : 1.f;
+        out[t * 128] = fmaf(g, v + bias, out[t * 128]);
+    };
+    // phase 2: token t's columns are t P ..; phase 3: those of its place in the mask
     if (Form<MODE>::P == 1) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(acc, r);
         tmem_ld_wait_regs(r);
         tc_fence_before();
         mbar_arrive(acce + buf);
+        uint32_t m = third ? j.mask : (1u << c.p.T) - 1u;
 #pragma unroll
         for (int i = 0; i < MAX_T; ++i) {
             if (!m) break;
-            body(__ffs(m) - 1, __uint_as_float(r[i]));
+            const int t = __ffs(m) - 1;
             m &= m - 1;
+            if (j.mask >> t & 1u) add(t, __uint_as_float(r[i]));
         }
     } else {
         // five columns a token (the load reads three more)
-        for (int i = 0; m; ++i, m &= m - 1) {
+        int i = 0;
+#pragma unroll 1
+        for (uint32_t m = j.mask; m; m &= m - 1, ++i) {
+            const int t = __ffs(m) - 1;
             uint32_t r[8];
-            tmem_ld_32x32b_x8(acc + static_cast<uint32_t>(PLANES * i), r);
+            tmem_ld_32x32b_x8(acc + static_cast<uint32_t>(PLANES * (third ? i : t)), r);
             tmem_ld_wait_regs(r);
             float v = __uint_as_float(r[PLANES - 1]);
 #pragma unroll
             for (int q = PLANES - 2; q >= 0; --q) v += __uint_as_float(r[q]);
-            body(__ffs(m) - 1, v);
+            add(t, v);
         }
         tc_fence_before();
         mbar_arrive(acce + buf);
     }
 }
 
-// A tile that crosses blocks: stores this block's sums (sums[t * 128] for the
-// thread's row, tokens of `mask`), and in the last of the tile's blocks to get
-// here replaces them by the total over the blocks, in block order.  True where
-// the sums are now the tile's.  Every epilogue thread calls it.
-__device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mask, float* sums) {
+// A tile that crosses shares: stores this share's sums (out_s[t * 128 + row],
+// the tokens of `mask`), and in the last of the tile's shares to get here
+// replaces them by the total, in the order of the shares.  True where the sums
+// are now the tile's.  Every epilogue thread calls it.
+__device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mask, float* out_s) {
     const FewParams& p = c.p;
-    if (j.block0 == j.block1) return true;
-    const int b = blockIdx.x;
-    // a block has at most one tile it continues and one it leaves unfinished
-    auto part = [&](int blk) { return p.sums + (static_cast<size_t>(blk) * 2 + (blk == j.block0)) * p.T * 128 + c.tid; };
-    float* mine = part(b);
+    if (j.share0 == j.share1) return true;
+    // a share has at most one tile it continues and one it leaves unfinished
+    auto part = [&](int s) { return p.sums + (static_cast<size_t>(s) * 2 + (s == j.share0)) * p.T * 128; };
+    float* mine = part(j.share);
+#pragma unroll 1
     for (uint32_t m = mask; m; m &= m - 1) {
-        const int t = __ffs(m) - 1;
-        __stcg(mine + t * 128, sums[t * 128]);
+        const int at = (__ffs(m) - 1) * 128 + c.tid;
+        __stcg(mine + at, out_s[at]);
     }
     int* last_s = reinterpret_cast<int*>(c.smem + OFF_MISC) + 3;
     __threadfence();
     bar_epilogue();
     if (c.tid == 0) {
-        uint32_t* ctr = p.ctr + CTR_TILE + j.block0;
-        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(j.block1 - j.block0);
+        uint32_t* ctr = p.ctr + CTR_TILE + j.share0;
+        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(j.share1 - j.share0);
         if (last) *ctr = 0;
         __threadfence();
         *last_s = last;
     }
     bar_epilogue();
-    const bool last = *last_s != 0;
-    bar_epilogue();                                            // the flag may be written again
-    if (!last) return false;
-    for (uint32_t m = mask; m; m &= m - 1) {
-        const int t = __ffs(m) - 1;
-        float v = 0.f;
-#pragma unroll 4
-        for (int blk = j.block0; blk <= j.block1; ++blk) v += __ldcg(part(blk) + t * 128);
-        sums[t * 128] = v;
+    if (!*last_s) {
+        bar_epilogue();                                        // the flag may be written again
+        return false;
     }
+    // four rows of a token a thread
+#pragma unroll 1
+    for (int i = c.tid; i < p.T * 32; i += EPI) {
+        if (!(mask >> (i / 32) & 1u)) continue;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = j.share0; s <= j.share1; ++s) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(part(s)) + i);
+            v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+        }
+        reinterpret_cast<float4*>(out_s)[i] = v;
+    }
+    bar_epilogue();
     return true;
 }
 
 // ---------------------------------------------------------------- phase 1
 
-// Router slices are at most 14 x 128 columns: a warp holds an expert's slice
-// in registers (14 float4 a lane, one round of loads) and runs the tokens past
-// it.
-constexpr int SLICE_PIECES = 14;
-
+// (A warp holds an expert's slice in registers, 14 float4 a lane in one round of
+// loads, and runs the tokens past it.)
 template <int MODE>
 __device__ __forceinline__ void router_and_x(const Ctx& c) {
     const FewParams& p = c.p;
@@ -684,49 +768,59 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
     if (who < sharers) {
         const int e0 = p.E * who / sharers, e1 = p.E * (who + 1) / sharers;
         const int k0 = ks * p.slice, len = min(p.slice, p.d - k0);       // multiples of 64
-        const int rounds = (len + 127) / 128;                            // (zeros up to the last one's end)
-        for (int i = c.tid; i < p.T * rounds * 16; i += CT) {
-            const int t = i / (rounds * 16), q = i - t * rounds * 16;
-            reinterpret_cast<uint4*>(xsm + t * p.slice)[q] = 8 * q < len
-                ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.d + k0) + q) : make_uint4(0, 0, 0, 0);
+        // a token's slice and zeros up to the width that a warp computes
+        constexpr int W8 = SLICE_PIECES * 16;
+#pragma unroll 1
+        for (int i = c.tid; i < p.T * W8; i += CT) {
+            const int t = i / W8, q = i - t * W8;
+            uint4* dst = reinterpret_cast<uint4*>(xsm) + i;
+            if (8 * q < len) cp_async_16(dst, reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.d + k0) + q);
+            else *dst = make_uint4(0, 0, 0, 0);
         }
+#pragma unroll 1
         for (int e = e0 + c.warp; e < e0 + (e1 - e0 + CW - 1) / CW * CW; e += CW) {
             float4 w[SLICE_PIECES];
             const float4* src = reinterpret_cast<const float4*>(p.W_r + static_cast<size_t>(min(e, p.E - 1)) * p.d + k0);
 #pragma unroll
             for (int i = 0; i < SLICE_PIECES; ++i)
                 w[i] = 32 * i + c.lane < len / 4 ? __ldg(src + 32 * i + c.lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e < e0 + CW) bar_general();                              // the slices of x are there
+            if (e < e0 + CW) {                                           // the slices of x are there
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                bar_general();
+            }
             if (e >= e1) continue;
 #pragma unroll 1
             for (int t = 0; t < p.T; ++t) {
-                float acc = 0.f;
+                const uint2* xt = reinterpret_cast<const uint2*>(xsm) + t * (2 * W8) + c.lane;
+                float acc[4] = {};                                       // one per element of a float4
 #pragma unroll
                 for (int i = 0; i < SLICE_PIECES; ++i) {
-                    if (i < rounds) {
-                        const uint2 xv = *reinterpret_cast<const uint2*>(xsm + t * p.slice + 4 * (32 * i + c.lane));
-                        acc = fmaf(__uint_as_float(xv.x << 16), w[i].x, acc);
-                        acc = fmaf(__uint_as_float(xv.x & 0xFFFF0000u), w[i].y, acc);
-                        acc = fmaf(__uint_as_float(xv.y << 16), w[i].z, acc);
-                        acc = fmaf(__uint_as_float(xv.y & 0xFFFF0000u), w[i].w, acc);
-                    }
+                    const uint2 xv = xt[32 * i];
+                    acc[0] = fmaf(__uint_as_float(xv.x << 16), w[i].x, acc[0]);
+                    acc[1] = fmaf(__uint_as_float(xv.x & 0xFFFF0000u), w[i].y, acc[1]);
+                    acc[2] = fmaf(__uint_as_float(xv.y << 16), w[i].z, acc[2]);
+                    acc[3] = fmaf(__uint_as_float(xv.y & 0xFFFF0000u), w[i].w, acc[3]);
                 }
+                float v = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-                if (c.lane == 0) p.part[(static_cast<size_t>(ks) * p.T + t) * p.E + e] = acc;
+                for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (c.lane == 0) p.part[(static_cast<size_t>(ks) * p.T + t) * p.e4 + e] = v;
             }
         }
     }
-    if (MODE != M_BF16) {
-        const int nb = p.d / 128;
-        for (int i = blockIdx.x * CW + c.warp; i < p.T * nb; i += gridDim.x * CW) {
-            const int t = i / nb, b = i % nb;
-            const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.d + b * 128) + c.lane);
-            store_block<MODE>(make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)),
-                              p.xq, p.xs, t, p.d, b * 128, c.lane);
-        }
+    // the image of x, a warp per 128 columns (bf16: d may end inside them)
+    const int nb = (p.d + 127) / 128;
+#pragma unroll 1
+    for (int i = blockIdx.x * CW + c.warp; i < p.T * nb; i += gridDim.x * CW) {
+        const int t = i / nb, col = (i - t * nb) * 128;
+        uint2 raw = make_uint2(0, 0);
+        if (MODE != M_BF16 || col + 4 * c.lane < p.d)
+            raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(t) * p.d + col) + c.lane);
+        store_block<MODE>(make_float4(__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                                      __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)),
+                          p.xq, p.xs, rows8<MODE>(p.T), t, col, c.lane);
     }
+    fence_proxy_async_all();                                   // read by bulk copies after the barrier
 }
 
 // ---------------------------------------------------------------- selection
@@ -740,6 +834,7 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 // Top-K, gates and the list of experts reached, by every block for itself (the
 // last block also keeps the probabilities, for balance()).  The number of
 // experts reached goes to the block's misc words.
+template <int MODE>
 __device__ __forceinline__ void select_experts(const Ctx& c) {
     const FewParams& p = c.p;
     int* idx_s = reinterpret_cast<int*>(c.smem + OFF_IDX);
@@ -749,22 +844,33 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
     int* act_s = reinterpret_cast<int*>(c.smem + OFF_ACT);
     int* misc = reinterpret_cast<int*>(c.smem + OFF_MISC);
     const bool writer = blockIdx.x == gridDim.x - 1;
-    for (int t = c.warp; t < p.T; t += CW) {
+    // the partial logits into the ring's memory at once (read by every block:
+    // a dependent read of the same few lines by all of them costs 2 us each)
+    float* part_s = reinterpret_cast<float*>(c.smem + OFF_RING);
+    const int chunk = min(p.T, static_cast<int>(RING_BYTES / 4) / (p.ks * p.e4));  // tokens that fit
+#pragma unroll 1
+    for (int t0 = 0; t0 < p.T; t0 += chunk) {
+        const int nt = min(chunk, p.T - t0), row = nt * p.e4 / 4;                  // float4 per slice
+        bar_general();
+#pragma unroll 1
+        for (int i = c.tid; i < p.ks * row; i += CT) {
+            const int s = i / row;
+            cp_async_16(part_s + 4 * i, p.part + (static_cast<size_t>(s) * p.T + t0) * p.e4 + 4 * (i - s * row));
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        bar_general();
+#pragma unroll 1
+        for (int t = t0 + c.warp; t < t0 + nt; t += CW) {
         float l[8];
         uint32_t key[8];
         float top = -INFINITY;
-        const float* part = p.part + static_cast<size_t>(t) * p.E;
+        const float* part = part_s + (t - t0) * p.e4;
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] = 0.f;
-        // every load of a round is issued before the first is used (experts past
-        // the last one read the last one's)
 #pragma unroll 2
         for (int s = 0; s < p.ks; ++s) {
-            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + s * p.T * p.E + min(32 * i + c.lane, p.E - 1));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) l[i] += v[i];
+            for (int i = 0; i < 8; ++i) l[i] += part[s * 4 * row + min(32 * i + c.lane, p.E - 1)];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -791,6 +897,7 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
             for (int i = 0; i < 8; ++i) p.prob[t * 256 + 32 * i + c.lane] = l[i] * inv;
         }
         float chosen = 0.f, mine = 0.f;
+#pragma unroll 1
         for (int k = 0; k < p.K; ++k) {
             uint32_t bk = 0, bi = 0xFFFFu;
 #pragma unroll
@@ -808,6 +915,7 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
             if (c.lane == 0) idx_s[t * 16 + k] = static_cast<int>(e);
         }
         if (c.lane < p.K) gate_s[t * 16 + c.lane] = mine / chosen;
+        }
     }
     mask_s[c.tid] = 0;
     kpack_s[c.tid] = 0;
@@ -831,7 +939,9 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
         uint32_t keep = 0;
         int left = p.capacity;
         const uint64_t kpack = kpack_s[e];
+#pragma unroll 1
         for (int k = 0; k < (p.slot_major ? p.K : 1); ++k)
+#pragma unroll 1
             for (uint32_t m = mask; m && left > 0; m &= m - 1) {
                 const int t = __ffs(m) - 1;
                 if (!p.slot_major || (static_cast<int>(kpack >> (4 * t)) & 15) == k) { keep |= 1u << t; --left; }
@@ -839,33 +949,52 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
         mask = keep;
         mask_s[e] = keep;
     }
+    // experts reached, in ascending order, and where their images of h start
     const uint32_t votes = __ballot_sync(0xffffffffu, mask != 0);
-    if (c.lane == 0) misc[4 + c.warp] = __popc(votes);
+    const int r8 = rows8<MODE>(__popc(mask));
+    int before = r8;                                           // inclusive sum over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (c.lane >= o) before += v;
+    }
+    if (c.lane == 31) {
+        misc[4 + c.warp] = __popc(votes);
+        misc[12 + c.warp] = before;
+    }
     bar_general();
-    int base = 0, total = 0;
+    int rank = __popc(votes & ((1u << c.lane) - 1u)), base8 = before - r8, total = 0;
 #pragma unroll
     for (int w = 0; w < CW; ++w) {
-        const int n = misc[4 + w];
-        if (w < c.warp) base += n;
-        total += n;
+        if (w < c.warp) {
+            rank += misc[4 + w];
+            base8 += misc[12 + w];
+        }
+        total += misc[4 + w];
     }
-    if (mask) act_s[base + __popc(votes & ((1u << c.lane) - 1u))] = e;
+    if (mask) {
+        act_s[rank] = e;
+        reinterpret_cast<int*>(c.smem + OFF_BASE)[e] = base8 | rank << 16;
+    }
     if (c.tid == 0) misc[1] = total;
 }
 
-// The routing outputs and the balance statistics, by the token-side threads of
-// the last block once they have no copies left to make.
+// The routing outputs and the balance statistics, by warps 4..7 of the last
+// block, which have nothing to do in phase 3.
 __device__ __forceinline__ void balance(const Ctx& c) {
     const FewParams& p = c.p;
     const int i = c.tid - EPI;
+#pragma unroll 1
     for (int s = i; s < p.T * p.K; s += EPI) {
         const int at = s / p.K * 16 + s % p.K;
         if (p.topk_idx) p.topk_idx[s] = reinterpret_cast<const int*>(c.smem + OFF_IDX)[at];
         if (p.gates) p.gates[s] = reinterpret_cast<const float*>(c.smem + OFF_GATE)[at];
     }
     float sum = 0.f;
+#pragma unroll 1
     for (int e = i; e < p.E; e += EPI) {
         float P = 0.f;
+#pragma unroll 1
         for (int t = 0; t < p.T; ++t) P += __ldcg(p.prob + t * 256 + e);
         P /= static_cast<float>(p.T);
         const int count = reinterpret_cast<const int*>(c.smem + OFF_COUNT)[e];
@@ -877,9 +1006,9 @@ __device__ __forceinline__ void balance(const Ctx& c) {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    float* red = reinterpret_cast<float*>(c.smem + OFF_MISC) + 4;         // the selection's counts
+    float* red = reinterpret_cast<float*>(c.smem + OFF_MISC) + 4;              // (the selection is over)
     if (c.lane == 0) red[c.warp - 4] = sum;
-    bar_tokens();
+    bar_upper();
     if (i == 0) *p.loss = p.alpha * p.E * (red[0] + red[1] + red[2] + red[3]);
 }
 
@@ -894,18 +1023,20 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* accf = full + 2 * MAX_SLOTS;
     uint64_t* acce = accf + 2;
-    uint64_t* drain = acce + 2;
     int* misc = reinterpret_cast<int*>(smem + OFF_MISC);
     const Ctx c{p, smem, full, full + MAX_SLOTS, misc, static_cast<int>(threadIdx.x),
                 static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31)};
     if (c.tid == 0) {
-        for (int i = 0; i < p.slots; ++i) {
-            // expect_tx; the token side's copies and, in FP8, stores
-            mbar_init(c.full + i, 1 + EPI * (MODE == M_FP8 ? 2 : 1));
+        for (int i = 0; i < MAX_SLOTS; ++i) {
+            mbar_init(c.full + i, 2);                           // weights, tokens
             mbar_init(c.empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) { mbar_init(accf + i, 1); mbar_init(acce + i, EPI); }
-        mbar_init(drain, 1);
+        mbar_init(full + 2 * MAX_SLOTS + 4, 1);
+        for (int i = 0; i < JOBS; ++i) {
+            mbar_init(JobQueue::full(c, i), 1);
+            mbar_init(JobQueue::empty(c, i), JOB_READERS);
+        }
         misc[0] = 0;
         fence_mbar_init();
     }
@@ -915,7 +1046,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(misc[2]);
 
-    if (c.warp == W_TMA) {
+    if (c.warp == W_LOAD) {
         if (c.lane == 0) {
             tma_prefetch_desc(&p.w1);
             tma_prefetch_desc(&p.w2);
@@ -924,115 +1055,172 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         __syncthreads();                                        // the experts are selected
         const int n_active = misc[1];
         Ring ring;
+        JobQueue queue;
         bool ok = *c.abort_flag == 0;
         Job j;
 #pragma unroll 1
-        for (int phase = 2; phase <= 3; ++phase)
-            for (Jobs<MODE> jobs(c, phase, n_active); ok && jobs.next(j);)
-                ok = load_weights<MODE>(c, j, phase == 2 ? (j.shared ? &p.ws1 : &p.w1) : (j.shared ? &p.ws2 : &p.w2), ring);
+        for (int phase = 2; phase <= 3; ++phase) {
+            const bool third = phase == 3;
+            Plan<MODE> plan(c, phase, n_active);
+            // the first share is the block's own, the others come off a counter,
+            // drawn a share ahead
+            int share = blockIdx.x;
+#pragma unroll 1
+            while (ok && share < plan.shares) {
+                int after = 0;
+                if (c.lane == 0) after = static_cast<int>(gridDim.x + atomicAdd(p.ctr + CTR_SHARE + phase - 2, 1u));
+                plan.take(share);
+#pragma unroll 1
+                while (ok && plan.next(j)) {
+                    const void* sc = third ? (j.shared ? p.ws2s : p.w2s) : (j.shared ? p.ws1s : p.w1s);
+                    ok = post<MODE>(c, queue, j, static_cast<const float*>(sc)) &&
+                         load_weights<MODE>(c, j, third ? (j.shared ? &p.ws2 : &p.w2) : (j.shared ? &p.ws1 : &p.w1),
+                                            static_cast<const uint8_t*>(sc), ring);
+                }
+                share = __shfl_sync(0xffffffffu, after, 0);
+            }
+            j.p0 = -1;
+            ok = ok && post<MODE>(c, queue, j, nullptr);
+        }
         // a block that gave up leaves its copies the time to land before it
-        // gives its memory back (their barriers may never complete, since the
-        // token side stopped arriving)
+        // gives its memory back (their barriers may never complete)
         if (!ok && c.lane == 0) {
             const uint64_t t0 = global_timer_ns();
             while (global_timer_ns() - t0 < kDrainNs) {}
         }
         __syncwarp();
+    } else if (c.warp == W_TOKENS) {
+        __syncthreads();
+        Ring ring;
+        JobQueue queue;
+        bool ok = *c.abort_flag == 0;
+        Job j;
+#pragma unroll 1
+        for (int phase = 2; phase <= 3; ++phase) {
+            if (phase == 3) bar_tokens_ready();
+            fence_proxy_async_all();                            // the images were written through the generic proxy
+            while (queue.next(c, j, ok)) {
+                queue.done(c);
+                ok = load_tokens<MODE>(c, j, phase == 3, ring);
+            }
+        }
     } else if (c.warp == W_MMA) {
         __syncthreads();
-        const int n_active = misc[1];
         MmaState st;
         st.leader = elect_one();
+        JobQueue queue;
         bool ok = *c.abort_flag == 0;
         Job j;
 #pragma unroll 1
         for (int phase = 2; phase <= 3; ++phase)
-            for (Jobs<MODE> jobs(c, phase, n_active); ok && jobs.next(j);) ok = issue_job<MODE>(c, j, tmem, accf, acce, st);
-        if (!ok && st.slots && st.leader) {
-            umma_commit(drain);
+            while (queue.next(c, j, ok)) {
+                ok = issue_job<MODE>(c, j, smem + OFF_JOBSC + queue.at * JOB_PIECES, phase == 3, tmem, accf, acce, st);
+                queue.done(c);
+            }
+        if (!ok && st.leader) {
+            umma_commit(full + 2 * MAX_SLOTS + 4);
             volatile int no_abort = 0;
-            mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainNs);
+            mbar_wait_bounded(full + 2 * MAX_SLOTS + 4, static_cast<uint32_t>(st.rewrites & 1), &no_abort, nullptr, kDrainNs);
         }
         __syncwarp();
     } else {
         router_and_x<MODE>(c);
         grid_barrier(p.ctr, 0, p.status, c.abort_flag, c.tid);
-        select_experts(c);
+        select_experts<MODE>(c);
         fence_proxy_async_smem();                               // phase 1 used the ring's memory
         __syncthreads();
-        const int n_active = misc[1];
         const int* idx_s = reinterpret_cast<const int*>(smem + OFF_IDX);
         const float* gate_s = reinterpret_cast<const float*>(smem + OFF_GATE);
         const uint32_t* mask_s = reinterpret_cast<const uint32_t*>(smem + OFF_MASK);
         const int slots_h = p.T * p.K;                          // rows of routed h
         const size_t h_shared = static_cast<size_t>(slots_h) * p.dff;
-        float* sums = reinterpret_cast<float*>(smem + OFF_OUT) + c.tid;            // epilogue: [t * 128]
-        Ring ring;
+        float* out_s = reinterpret_cast<float*>(smem + OFF_OUT);                   // [T][128]
+        float* sums = out_s + c.tid;                                               // epilogue: this thread's row
+        JobQueue queue;
         int jobs_read = 0;
         bool ok = *c.abort_flag == 0;
 #pragma unroll 1
         for (int phase = 2; phase <= 3; ++phase) {
             const bool third = phase == 3;
             if (third) {
+                if (MODE == M_BF16) fence_proxy_async_all();    // phase 2 wrote the image
                 grid_barrier(p.ctr, 1, p.status, c.abort_flag, c.tid);
                 if (MODE != M_BF16) {
-                    // h in operand form, a warp per 128 values that phase 3
-                    // reads; a slot over the capacity has none
-                    constexpr int P = Form<MODE>::P;
+                    // the image of h, a warp per 128 values; a slot over the
+                    // capacity has none
                     const int nr = p.dff / 128, ns = p.dffs / 128;
                     const int routed = slots_h * nr, blocks = routed + p.S * p.T * ns;
-                    uint8_t* hq_shared = p.hq + h_shared * P / (MODE == M_FP4 ? 2 : 1);
-                    uint8_t* hs_shared = p.hs + (MODE == M_FP4 ? h_shared * P / 32 : h_shared / 128 * 4);
+#pragma unroll 1
                     for (int i = blockIdx.x * CW + c.warp; i < blocks; i += gridDim.x * CW) {
                         const bool sh = i >= routed;
-                        const int u = sh ? i - routed : i, nb = sh ? ns : nr, row = u / nb, col = u % nb * 128;
-                        const int t = row / p.K;
-                        if (!sh && !(mask_s[idx_s[t * 16 + row - t * p.K]] >> t & 1u)) continue;
-                        const int k = sh ? p.dffs : p.dff;
+                        const int u = sh ? i - routed : i, nb = sh ? ns : nr, row = u / nb, col = (u - row * nb) * 128;
+                        const int k = sh ? p.dffs : p.dff, pieces = pieces_of<MODE>(k);
                         const float4 v = __ldcg(reinterpret_cast<const float4*>(
                             p.h32 + (sh ? h_shared : 0) + static_cast<size_t>(row) * k + col) + c.lane);
-                        store_block<MODE>(v, sh ? hq_shared : p.hq, sh ? hs_shared : p.hs, row, k, col, c.lane);
+                        if (sh) {
+                            const int s = row / p.T, r8 = rows8<MODE>(p.T);
+                            store_block<MODE>(v, p.hqs + static_cast<size_t>(s * r8) * pieces * 1024,
+                                              p.hss + static_cast<size_t>(s) * pieces * Form<MODE>::SFB, r8, row - s * p.T, col,
+                                              c.lane);
+                            continue;
+                        }
+                        const int t = row / p.K, e = idx_s[t * 16 + row - t * p.K];
+                        const uint32_t m = mask_s[e];
+                        if (!(m >> t & 1u)) continue;
+                        const int base = reinterpret_cast<const int*>(smem + OFF_BASE)[e];
+                        store_block<MODE>(v, p.hq + static_cast<size_t>(base & 0xFFFF) * pieces * 1024,
+                                          p.hs + static_cast<size_t>(base >> 16) * pieces * Form<MODE>::SFB,
+                                          rows8<MODE>(__popc(m)), __popc(m & ((1u << t) - 1u)), col, c.lane);
                     }
+                    fence_proxy_async_all();
                     grid_barrier(p.ctr, 2, p.status, c.abort_flag, c.tid);
                 }
+                bar_tokens_ready();
                 ok = ok && *c.abort_flag == 0;
             }
             if (c.warp >= 4) {
-                load_tokens<MODE>(c, phase, n_active, h_shared, ring, ok);
                 if (third && blockIdx.x == gridDim.x - 1) balance(c);
                 continue;
             }
             bool begins = true;
             Job j;
-            for (Jobs<MODE> jobs(c, phase, n_active); jobs.next(j);) {
-                if (begins) for (int t = 0; t < p.T; ++t) sums[t * 128] = 0.f;
+            while (queue.next(c, j, ok)) {
+                queue.done(c);
+                if (begins) {
+#pragma unroll 1
+                    for (int t = 0; t < p.T; ++t) sums[t * 128] = 0.f;
+                }
                 begins = j.ends;
                 const int row = j.row0 + c.tid;
                 const bool in = row < j.n;
-                // phase 3: the block with a matrix's first piece adds its bias
+                // phase 3: the share with a matrix's first piece adds its bias
                 const float* biases = third ? (j.shared ? p.bs2 : p.b2) : (j.shared ? p.bs1 : p.b1);
                 const float bias = in && (!third || j.p0 == 0) ? __ldg(biases + static_cast<size_t>(j.mat) * j.n + row) : 0.f;
-                const bool gated = third && !j.shared;
-                const float inner = third ? bias : 0.f;
-                read_job<MODE>(c, j, tmem, accf, acce, jobs_read, ok, [&](int t, float v) {
-                    const float g = gated ? gate_s[t * 16 + (static_cast<int>(j.kpack >> (4 * t)) & 15)] : 1.f;
-                    sums[t * 128] = fmaf(g, v + inner, sums[t * 128]);
-                });
+                read_job<MODE>(c, j, third, third ? bias : 0.f, tmem, accf, acce, jobs_read, ok, sums);
                 const uint32_t tokens = third ? (1u << p.T) - 1u : j.mask;
-                if (!j.ends || !combine(c, j, tokens, sums) || !in || !ok) continue;
-                const size_t base = j.shared ? h_shared : 0;
+                if (!j.ends || !combine(c, j, tokens, out_s) || !in || !ok) continue;
+#pragma unroll 1
                 for (uint32_t m = tokens; m; m &= m - 1) {
                     const int t = __ffs(m) - 1;
                     float v = sums[t * 128];
                     if (!third) {
                         const float h = silu_fast(v + bias);
-                        const size_t at = base + static_cast<size_t>(h_row(c, j, t)) * j.n + row;
-                        if (MODE == M_BF16) reinterpret_cast<__nv_bfloat16*>(p.hq)[at] = __float2bfloat16_rn(h);
-                        else p.h32[at] = h;
+                        if (MODE == M_BF16) {
+                            // two bytes of row (the token's place) of a piece
+                            const int n = column_of(j, t), at = 2 * row;
+                            const size_t piece = static_cast<size_t>(j.base8) * pieces_of<MODE>(j.n) +
+                                                 static_cast<size_t>(at >> 7) * rows8<MODE>(__popc(j.mask));
+                            uint8_t* dst = (j.shared ? p.hqs : p.hq) + (piece + (n >> 3)) * 1024 + (n & 7) * 128 +
+                                           ((((at >> 4) & 7) ^ (n & 7)) << 4) + (at & 15);
+                            *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(h);
+                        } else {
+                            p.h32[(j.shared ? h_shared : 0) + static_cast<size_t>(h_row(c, j, t)) * j.n + row] = h;
+                        }
                         continue;
                     }
                     const size_t at = static_cast<size_t>(t) * p.d + row;
                     if (p.passthrough) {
+#pragma unroll 1
                         for (int k = 0; k < p.K; ++k)
                             if (!(mask_s[idx_s[t * 16 + k]] >> t & 1u))
                                 v = fmaf(gate_s[t * 16 + k], __bfloat162float(p.x[at]), v);
@@ -1044,10 +1232,17 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
     }
     tc_fence_before();
     __syncthreads();
-    // the last block to leave zeroes the counters for the next launch
+    // the last block to leave zeroes the counters for the next launch (a
+    // tile's own are zero again unless a block gave up)
     if (c.tid == 0) {
+        if (*c.abort_flag) atomicExch(p.ctr + CTR_ABORT, 1u);
         __threadfence();
         if (atomicAdd(p.ctr + CTR_EXIT, 1u) == gridDim.x - 1) {
+            __threadfence();
+            if (ld_acquire(p.ctr + CTR_ABORT))
+#pragma unroll 1
+                for (unsigned i = 0; i < SHARES * gridDim.x; ++i) p.ctr[CTR_TILE + i] = 0;
+#pragma unroll 1
             for (int i = 0; i < CTR_WORDS; ++i) p.ctr[i] = 0;
             __threadfence();
         }
@@ -1061,7 +1256,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 struct FewLayout {
-    size_t ctr, part, prob, xq, xs, h32, hq, hs, sums, total;
+    size_t ctr, part, prob, xq, xs, hq, hs, hqs, hss, h32, sums, total;
 };
 
 // blocks: as many as can find work, at most one per SM
@@ -1073,9 +1268,11 @@ FewPlan few_plan(const Dims& dm, int sms) {
     FewPlan f;
     if (sms > MAX_BLOCKS) sms = MAX_BLOCKS;
     // a block per slot of weights that the most experts reached would have
-    const int kp = dm.dtype == MOE_BF16 ? Form<M_BF16>::KP : dm.dtype == MOE_MXFP4 ? Form<M_FP4>::KP : Form<M_FP8>::KP;
-    auto slots = [&](long long rows, long long k) { return (rows + 127) / 128 * ((k + NP * kp - 1) / (NP * kp)); };
     const long long reached = dm.T * dm.K < dm.E ? dm.T * dm.K : dm.E;
+    auto slots = [&](long long rows, int k) {
+        return (rows + 127) / 128 * (dm.dtype == MOE_BF16 ? slots_of<M_BF16>(k) : dm.dtype == MOE_MXFP4 ? slots_of<M_FP4>(k)
+                                                                                                     : slots_of<M_FP8>(k));
+    };
     const long long s2 = reached * slots(dm.dff, dm.d) + dm.S * slots(dm.dffs, dm.d);
     const long long s3 = reached * slots(dm.d, dm.dff) + dm.S * slots(dm.d, dm.dffs);
     const long long most = s2 > s3 ? s2 : s3;
@@ -1096,36 +1293,44 @@ FewPlan few_plan(const Dims& dm, int sms) {
     return f;
 }
 
-FewLayout few_layout(const Dims& dm) {
+template <int MODE>
+FewLayout few_layout_mode(const Dims& dm) {
     FewLayout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off = align256(off + bytes); return o; };
-    const bool q = dm.dtype != MOE_BF16, fp4 = dm.dtype == MOE_MXFP4;
+    const bool q = MODE != M_BF16;
     const size_t h = static_cast<size_t>(dm.T) * dm.K * dm.dff + static_cast<size_t>(dm.S) * dm.T * dm.dffs;
-    const size_t x = static_cast<size_t>(dm.T) * dm.d;
-    // bytes of n elements in operand form, and of their scales
-    auto form = [&](size_t n) { return fp4 ? n * PLANES / 2 : q ? n : 2 * n; };
-    auto scales = [&](size_t n) { return fp4 ? n * PLANES / 32 : q ? n / 128 * 4 : 0; };
+    auto pieces = [](int k) { return static_cast<size_t>(pieces_of<MODE>(k)); };
     take(256);                                              // status word
-    L.ctr = take((CTR_TILE + MAX_BLOCKS) * 4);
+    L.ctr = take((CTR_TILE + SHARES * MAX_BLOCKS) * 4);
     // slices are at least 128 columns long, whatever the device's size
-    L.part = take(static_cast<size_t>((dm.d + 127) / 128) * dm.T * dm.E * 4);
+    L.part = take(static_cast<size_t>((dm.d + 127) / 128) * dm.T * ((dm.E + 3) & ~3) * 4);
     L.prob = take(static_cast<size_t>(dm.T) * 256 * 4);
-    L.xq = take(q ? form(x) : 0);
-    L.xs = take(scales(x));
+    // images: the groups of 8 rows of T K slots over the experts reached are
+    // at most (T K P + 7 experts) / 8
+    const size_t reached = dm.T * dm.K < dm.E ? dm.T * dm.K : dm.E;
+    const size_t groups = (static_cast<size_t>(dm.T) * dm.K * Form<MODE>::P + 7 * reached) / 8;
+    L.xq = take(pieces(dm.d) * rows8<MODE>(dm.T) * 1024);
+    L.xs = take(pieces(dm.d) * Form<MODE>::SFB);
+    L.hq = take(pieces(dm.dff) * groups * 1024);
+    L.hs = take(pieces(dm.dff) * reached * Form<MODE>::SFB);
+    L.hqs = take(pieces(dm.dffs) * dm.S * rows8<MODE>(dm.T) * 1024);
+    L.hss = take(pieces(dm.dffs) * dm.S * Form<MODE>::SFB);
     L.h32 = take(q ? h * 4 : 0);
-    L.hq = take(form(h));
-    L.hs = take(scales(h));
-    L.sums = take(static_cast<size_t>(MAX_BLOCKS) * 2 * dm.T * 128 * 4);
+    L.sums = take(static_cast<size_t>(SHARES) * MAX_BLOCKS * 2 * dm.T * 128 * 4);
     L.total = off;
     return L;
 }
 
+FewLayout few_layout(const Dims& dm) {
+    return dm.dtype == MOE_BF16 ? few_layout_mode<M_BF16>(dm)
+           : dm.dtype == MOE_MXFP4 ? few_layout_mode<M_FP4>(dm) : few_layout_mode<M_FP8>(dm);
+}
+
 template <int MODE>
 cudaError_t launch_mode(FewParams& p, int blocks, cudaStream_t st) {
-    constexpr int rows_max = round16(MAX_T * Form<MODE>::P) * 128;
-    static_assert(RING_BYTES / (NP * (PIECE_BYTES + rows_max + Form<MODE>::SF)) >= 3, "two slots of MMAs in flight");
-    p.slot_bytes = NP * (PIECE_BYTES + round16(p.T * Form<MODE>::P) * 128 + Form<MODE>::SF);
+    static_assert(RING_BYTES / (sfa_at<MODE>(MAX_T) + NP * Form<MODE>::SFA) >= 3, "two slots of MMAs in flight");
+    p.slot_bytes = sfa_at<MODE>(p.T) + NP * Form<MODE>::SFA;
     p.slots = RING_BYTES / p.slot_bytes < MAX_SLOTS ? RING_BYTES / p.slot_bytes : MAX_SLOTS;
     auto kernel = few_tokens_kernel<MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
@@ -1178,16 +1383,19 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     p.ctr = reinterpret_cast<uint32_t*>(w + L.ctr);
     p.part = reinterpret_cast<float*>(w + L.part);
     p.prob = reinterpret_cast<float*>(w + L.prob);
-    p.xq = dm.dtype == MOE_BF16 ? const_cast<uint8_t*>(static_cast<const uint8_t*>(a.x)) : w + L.xq;
+    p.xq = w + L.xq;
     p.xs = w + L.xs;
-    p.h32 = reinterpret_cast<float*>(w + L.h32);
     p.hq = w + L.hq;
     p.hs = w + L.hs;
+    p.hqs = w + L.hqs;
+    p.hss = w + L.hss;
+    p.h32 = reinterpret_cast<float*>(w + L.h32);
     p.sums = reinterpret_cast<float*>(w + L.sums);
     p.alpha = dm.alpha;
     p.T = dm.T;
     p.d = dm.d;
     p.E = dm.E;
+    p.e4 = (dm.E + 3) & ~3;
     p.K = dm.K;
     p.dff = dm.dff;
     p.S = dm.S;

@@ -187,6 +187,8 @@ cudaError_t launch_mxfp4_quantize(const void* x, int dtype, long long elems, uin
                                   cudaStream_t st);
 cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, long long elems, void* out,
                                     int dtype, cudaStream_t st);
+cudaError_t launch_mxfp4_tile_scales(const uint8_t* scales, long long n_mats, int rows, int cols, uint8_t* tiled,
+                                     cudaStream_t st);
 cudaError_t launch_mxfp4_matmul(const moe_mxfp4_shape& s, const uint8_t* a, const uint8_t* a_scales,
                                 const int32_t* seg_offsets, const int32_t* seg_mat, const uint8_t* w,
                                 const uint8_t* w_scales, const float* bias, void* y, uint8_t* y_scales,

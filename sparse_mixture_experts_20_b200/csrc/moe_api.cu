@@ -608,6 +608,18 @@ int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t ro
     return cuda_status(launch_mxfp4_dequantize(codes, scales, elems, out, dtype, static_cast<cudaStream_t>(stream)));
 }
 
+int moe_mxfp4_tile_scales(const uint8_t* scales, int64_t n_mats, int32_t rows, int32_t cols, uint8_t* tiled,
+                          void* stream) {
+    NvtxRange nvtx("moe_mxfp4_tile_scales");
+    if (n_mats < 0 || rows < 1 || cols < 1) return MOE_ERR_INVALID_ARG;
+    if (cols % 128) return MOE_ERR_UNSUPPORTED;
+    const long long per = (static_cast<long long>(rows) + 127) / 128 * cols;     // words of a matrix
+    if (n_mats > (1ll << 38) / per) return MOE_ERR_UNSUPPORTED;
+    if (n_mats == 0) return MOE_OK;
+    if (!scales || !tiled || !aligned16(scales) || !aligned16(tiled)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_mxfp4_tile_scales(scales, n_mats, rows, cols, tiled, static_cast<cudaStream_t>(stream)));
+}
+
 static int mxfp4_validate(const moe_mxfp4_shape* s) {
     if (!s || s->rows < 0 || s->n < 1 || s->k < 1 || s->n_mats < 1 || s->n_seg < 1) return MOE_ERR_INVALID_ARG;
     if (s->activation != MOE_ACT_NONE && s->activation != MOE_ACT_SILU) return MOE_ERR_INVALID_ARG;

@@ -125,7 +125,34 @@ mxfp4_dequantize_kernel(const uint32_t* __restrict__ codes, const uint8_t* __res
     }
 }
 
+// A thread per word of the tiled scales: word w of row r of a tile of 128 rows
+// lies at 16 (r mod 32) + 4 (r div 32) of the tile's w-th 512 bytes.
+__global__ void __launch_bounds__(THREADS)
+mxfp4_tile_scales_kernel(const uint32_t* __restrict__ scales, long long total, int rows, int words, int tiles,
+                         uint32_t* __restrict__ out) {
+    pdl_wait();
+    pdl_allow_next();
+    const long long i = static_cast<long long>(blockIdx.x) * THREADS + threadIdx.x;
+    if (i >= total) return;
+    const int lane = static_cast<int>(i & 127);
+    const long long block = i >> 7;                        // (matrix, tile, word)
+    const int w = static_cast<int>(block % words);
+    const long long t = block / words;
+    const int row = static_cast<int>(t % tiles) * 128 + (lane >> 2) + 32 * (lane & 3);
+    // rows past the end: 2^0
+    out[i] = row < rows ? __ldg(scales + (t / tiles * rows + row) * words + w) : 0x7F7F7F7Fu;
+}
+
 }  // namespace
+
+cudaError_t launch_mxfp4_tile_scales(const uint8_t* scales, long long n_mats, int rows, int cols, uint8_t* tiled,
+                                     cudaStream_t st) {
+    const int words = cols / 128, tiles = (rows + 127) / 128;
+    const long long total = n_mats * tiles * words * 128;
+    const dim3 grid(static_cast<unsigned>((total + THREADS - 1) / THREADS));
+    return launch_pdl(mxfp4_tile_scales_kernel, grid, dim3(THREADS), 0, st, 1, reinterpret_cast<const uint32_t*>(scales),
+                      total, rows, words, tiles, reinterpret_cast<uint32_t*>(tiled));
+}
 
 cudaError_t launch_mxfp4_quantize(const void* x, int dtype, long long elems, uint8_t* codes, uint8_t* scales,
                                   cudaStream_t st) {
