@@ -97,6 +97,7 @@ struct Job {
     uint64_t kpack;              // routed: the tokens' slots, 4 bits each
     int ends;                    // the share's last job of this tile
     int share, share0, share1;   // this share, and the first and last with slots of the tile
+    int small0, smalls;          // and small shares of the tile alone, from small0 on
     int base8;                   // phase 3: first row of the expert's image, in units of 8
     int rank;                    // phase 3: its place among the experts reached (shared: its number)
 };
@@ -180,6 +181,10 @@ __device__ __forceinline__ void bar_tokens_ready() { asm volatile("bar.sync 4, %
 // Orders generic-proxy writes of global memory with async-proxy (bulk copy)
 // reads of it: by the writer before the barrier, by the reader after it.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -320,48 +325,86 @@ __device__ __forceinline__ int column_of(const Job& j, int t) { return __popc(j.
 // The shares of a phase's slots and their jobs (planning warp).  Phase 2:
 // matrix by matrix, its tiles, their slots of K = d.  Phase 3: tile by tile,
 // the shared experts' slots, then those of the experts reached.
+//
+// Fewer than 64 slots a block: equal shares, none without slots (the join of a
+// further share costs more than it evens out); in phase 2 of whole tiles, which
+// need no join, where that leaves no block more than 1/16 over its share.
+// Else phase 2 has three quarters
+// in a large share per block and the rest, at the end of the sequence, in small
+// ones of 12 slots or more.  Phase 3 has few tiles, and one cut into many
+// shares would be long to add up: there the last eighth of every tile is small
+// shares of its own, of 10 slots or more.
 template <int MODE>
 struct Plan {
     const Ctx& c;
     bool third;           // phase 3
     int share, shares, at, end;
-    int lead;             // slots of the large shares, one per block (0: none)
-    int each, extra;      // slots of the others; the first `extra` have one more
+    int lead;             // phase 2: slots of the large shares, one per block (0: none)
+    int each, extra;      // slots of the equal shares; the first `extra` have one more
     int ss, sr;           // slots of a shared, a routed matrix per tile
     int ts, tr;           // phase 2: tiles of a shared, a routed matrix
-    int tile;             // phase 3: slots of a tile
+    int head, tail, q;    // phase 3: a tile's slots in equal shares and in q small ones
+    int equal;            // phase 3: number of equal shares
+    int rest = 0;         // phase 2, whole tiles: tiles of the last share, if fewer
     __device__ __forceinline__ Plan(const Ctx& c_, int phase, int n_active) : c(c_), third(phase == 3) {
         const FewParams& p = c.p;
+        const int blocks = gridDim.x;
         ss = slots_of<MODE>(third ? p.dffs : p.d);
         sr = slots_of<MODE>(third ? p.dff : p.d);
         ts = third ? 1 : (p.dffs + 127) / 128;
         tr = third ? 1 : (p.dff + 127) / 128;
-        tile = third ? p.S * ss + n_active * sr : 1;
-        const int all = third ? (p.d + 127) / 128 * tile : (p.S * ts + n_active * tr) * sr;
-        // Fewer than 64 slots a block: equal shares (none without slots; the
-        // join of a further share costs more than it evens out).  Else three
-        // quarters in large shares and the rest in small ones of 12 slots or more.
-        const int blocks = gridDim.x, per = all / blocks;
-        lead = per < 64 ? 0 : 3 * per / 4;
-        const int others = lead ? blocks * max(1, min(SMALL, (per - lead) / 12)) : min(blocks, all);
-        shares = others + (lead ? blocks : 0);
-        each = (all - blocks * lead) / others;
-        extra = all - blocks * lead - each * others;
         at = end = 0;
+        lead = q = tail = 0;
+        head = 1;
+        if (!third) {
+            const int tiles = p.S * ts + n_active * tr, all = tiles * sr, per = all / blocks;
+            const int most = (tiles + blocks - 1) / blocks;    // tiles of a block, whole ones
+            equal = 0;
+            lead = per < 64 ? 0 : 3 * per / 4;
+            if (!lead && 16 * most * blocks <= 17 * tiles) {
+                shares = tiles / most;
+                each = most * sr;
+                extra = 0;
+                // (the rest of the tiles, fewer than a share's, go to a last share)
+                rest = tiles - shares * most;
+                if (rest) ++shares;
+            } else {
+                const int others = lead ? blocks * max(1, min(SMALL, (per - lead) / 12)) : min(blocks, all);
+                shares = others + (lead ? blocks : 0);
+                each = (all - blocks * lead) / others;
+                extra = all - blocks * lead - each * others;
+            }
+        } else {
+            const int tiles = (p.d + 127) / 128, tile = p.S * ss + n_active * sr;
+            if (tiles * tile / blocks >= 64) {
+                tail = tile / 8;
+                q = min(tail / 10, min(SMALL * blocks / tiles, (4 * blocks + tiles - 1) / tiles));
+                if (q < 1) q = tail = 0;
+            }
+            head = tile - tail;
+            equal = min(blocks, tiles * head);
+            each = tiles * head / equal;
+            extra = tiles * head - each * equal;
+            shares = equal + tiles * q;
+        }
     }
     __device__ __forceinline__ void take(int s) {
         share = s;
         const int blocks = gridDim.x;
-        if (lead && s < blocks) {
+        if (third && s >= equal) {
+            const int i = (s - equal) % q;
+            at = tail * i / q;
+            end = tail * (i + 1) / q;
+        } else if (!third && lead && s < blocks) {
             at = s * lead;
             end = at + lead;
         } else {
             const int v = lead ? s - blocks : s;
             at = blocks * lead + v * each + min(v, extra);
-            end = at + each + (v < extra ? 1 : 0);
+            end = rest && s == shares - 1 ? at + rest * sr : at + each + (v < extra ? 1 : 0);
         }
     }
-    // the share that has slot u
+    // the share that has slot u (phase 3: of the equal ones)
     __device__ __forceinline__ int share_of(int u) const {
         const int blocks = gridDim.x;
         if (u < blocks * lead) return u / lead;
@@ -373,12 +416,19 @@ struct Plan {
     __device__ __forceinline__ bool next(Job& j) {
         if (at >= end) return false;
         const FewParams& p = c.p;
-        int u = at, first = 0;
+        // u: slot of the tile (phase 3) or of the sequence; first .. last: the tile's slots of it
+        int u = at, first = 0, left = end - at, tile = 0;
         if (third) {
-            const int t = u / tile;
-            j.row0 = t * 128;
-            first = t * tile;
-            u -= first;
+            if (share >= equal) {
+                tile = (share - equal) / q;
+                u += head;
+            } else {
+                tile = u / head;
+                first = tile * head;
+                u -= first;
+                left = min(left, head - u);
+            }
+            j.row0 = tile * 128;
         }
         const int n_shared = p.S * ts * ss;
         j.shared = u < n_shared;
@@ -390,7 +440,7 @@ struct Plan {
             j.row0 = (run - m * tiles) * 128;
             first = at - s0;
         }
-        const int n = min(min(per - s0, end - at), JOB_PIECES / NP);
+        const int n = min(min(per - s0, left), JOB_PIECES / NP);
         j.mat = j.shared ? m : reinterpret_cast<const int*>(c.smem + OFF_ACT)[m];
         j.mask = j.shared ? (1u << p.T) - 1u : reinterpret_cast<const uint32_t*>(c.smem + OFF_MASK)[j.mat];
         j.kpack = j.shared ? 0 : reinterpret_cast<const uint64_t*>(c.smem + OFF_KPACK)[j.mat];
@@ -403,11 +453,13 @@ struct Plan {
         j.p0 = s0 * NP;
         j.p1 = min((s0 + n) * NP, (j.k + Form<MODE>::KP - 1) / Form<MODE>::KP);
         at += n;
-        const int last = first + (third ? tile : per) - 1;
-        j.ends = at == end || at > last;
+        j.ends = at == end || (third ? n == left : at == first + per);
         j.share = share;
-        j.share0 = share_of(first);
-        j.share1 = share_of(last);
+        const int f = third ? tile * head : first;
+        j.share0 = share_of(f);
+        j.share1 = share_of(f + (third ? head : per) - 1);
+        j.small0 = equal + tile * q;
+        j.smalls = q;
         return true;
     }
 };
@@ -454,37 +506,36 @@ template <int MODE> __host__ __device__ constexpr int sfa_at(int T) { return sfb
 
 // ---------------------------------------------------------------- planning and weights (one warp)
 
-// Announces a job; FP8: with the UE8M0 bytes of its pieces' weight scales.
+// Announces a job and loads its weights, and their scales: MXFP4 512 bytes per
+// 128 rows and 128 columns, tile by tile; FP8 the UE8M0 byte of each piece,
+// beside the announced job.  The bytes are on their way from HBM while the job
+// is announced and its first slots are loaded: the first slot's arrival is held
+// back until they are stored, which is when the MMA warp may read them.
 template <int MODE>
-__device__ __forceinline__ bool post(const Ctx& c, JobQueue& q, const Job& j, const float* scales) {
-    uint32_t s[JOB_PIECES / 32] = {};
-    if (MODE == M_FP8 && j.p0 >= 0) {
-        const float* row = scales + (static_cast<size_t>(j.mat) * (j.n / 128) + j.row0 / 128) * (j.k / 128) + j.p0;
-#pragma unroll
-        for (int i = 0; i < JOB_PIECES / 32; ++i)
-            if (32 * i + c.lane < j.p1 - j.p0) s[i] = (__float_as_uint(__ldg(row + 32 * i + c.lane)) >> 23) & 0xFFu;
-    }
-    if (!wait_warp(JobQueue::empty(c, q.at), q.phase ^ 1u, c)) return false;
-    if (MODE == M_FP8) {
-#pragma unroll
-        for (int i = 0; i < JOB_PIECES / 32; ++i)
-            c.smem[OFF_JOBSC + q.at * JOB_PIECES + 32 * i + c.lane] = static_cast<uint8_t>(s[i]);
-    }
-    if (c.lane == 0) *JobQueue::job(c, q.at) = j;
-    __syncwarp();
-    if (c.lane == 0) mbar_arrive(JobQueue::full(c, q.at));
-    q.step();
-    return true;
-}
-
-// Loads a job's weights, and their MXFP4 scales: 512 bytes per 128 rows and
-// 128 columns, tile by tile.
-template <int MODE>
-__device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const CUtensorMap* map, const uint8_t* scales,
-                                             Ring& ring) {
+__device__ __forceinline__ bool load_job(const Ctx& c, JobQueue& q, const Job& j, const CUtensorMap* map, const void* scales,
+                                         Ring& ring) {
     constexpr int ELEMS = MODE == M_BF16 ? 64 : 128;        // map elements (bf16, or bytes) per piece
     const int words = j.k / 128;
-    const uint8_t* sc = scales + (static_cast<size_t>(j.mat) * ((j.n + 127) / 128) + j.row0 / 128) * words * 512;
+    const size_t tile = static_cast<size_t>(j.mat) * ((j.n + 127) / 128) + j.row0 / 128;
+    const uint8_t* sc = static_cast<const uint8_t*>(scales) + tile * words * 512;
+    float f[JOB_PIECES / 32] = {};
+    if (MODE == M_FP8) {
+        const float* row = static_cast<const float*>(scales) + tile * words + j.p0;
+#pragma unroll
+        for (int i = 0; i < JOB_PIECES / 32; ++i)
+            if (32 * i + c.lane < j.p1 - j.p0) f[i] = __ldg(row + 32 * i + c.lane);
+    }
+    if (!wait_warp(JobQueue::empty(c, q.at), q.phase ^ 1u, c)) return false;
+    uint8_t* bytes = c.smem + OFF_JOBSC + q.at * JOB_PIECES;
+    if (c.lane == 0) {
+        *JobQueue::job(c, q.at) = j;
+        mbar_arrive(JobQueue::full(c, q.at));
+    }
+    __syncwarp();
+    q.step();
+    uint64_t* held = c.full + ring.slot;
+    // after the first two slots, or the only one
+    const int store_after = MODE == M_FP8 ? min(j.p0 + NP, (j.p1 - 1) / NP * NP) : -1;
 #pragma unroll 1
     for (int s = j.p0; s < j.p1; s += NP) {
         if (!wait_warp(c.empty + ring.slot, ring.phase ^ 1u, c)) return false;
@@ -493,14 +544,35 @@ __device__ __forceinline__ bool load_weights(const Ctx& c, const Job& j, const C
         const int np = min(NP, j.p1 - s);
         const uint32_t sfa = MODE == M_FP4 ? 512u * min(2 * NP, words - 2 * s) : 0u;
         if (c.lane == 0) {
-            mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * PIECE_BYTES) + sfa);
+            const uint32_t tx = static_cast<uint32_t>(np * PIECE_BYTES) + sfa;
+            if (MODE == M_FP8 && s == j.p0) mbar_expect_tx(full, tx);
+            else mbar_arrive_expect_tx(full, tx);
             tma_load_3d(slot, map, full, s * ELEMS, j.row0, j.mat);
             if (np > 1) tma_load_3d(slot + PIECE_BYTES, map, full, (s + 1) * ELEMS, j.row0, j.mat);
             if (MODE == M_FP4) bulk_load(slot + sfa_at<MODE>(c.p.T), sc + static_cast<size_t>(s) * 1024, sfa, full);
         }
         __syncwarp();
         ring.next(c.p.slots);
+        if (MODE == M_FP8 && s == store_after) {
+#pragma unroll
+            for (int i = 0; i < JOB_PIECES / 32; ++i)
+                bytes[32 * i + c.lane] = static_cast<uint8_t>((__float_as_uint(f[i]) >> 23) & 0xFFu);
+            __syncwarp();
+            if (c.lane == 0) mbar_arrive(held);
+        }
     }
+    return true;
+}
+
+// Announces the end of a phase.
+__device__ __forceinline__ bool end_phase(const Ctx& c, JobQueue& q) {
+    if (!wait_warp(JobQueue::empty(c, q.at), q.phase ^ 1u, c)) return false;
+    if (c.lane == 0) {
+        JobQueue::job(c, q.at)->p0 = -1;
+        mbar_arrive(JobQueue::full(c, q.at));
+    }
+    __syncwarp();
+    q.step();
     return true;
 }
 
@@ -714,7 +786,8 @@ __device__ __forceinline__ void read_job(const Ctx& c, const Job& j, bool third,
 // are now the tile's.  Every epilogue thread calls it.
 __device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mask, float* out_s) {
     const FewParams& p = c.p;
-    if (j.share0 == j.share1) return true;
+    const int parts = j.share1 - j.share0 + 1 + j.smalls;
+    if (parts == 1) return true;
     // a share has at most one tile it continues and one it leaves unfinished
     auto part = [&](int s) { return p.sums + (static_cast<size_t>(s) * 2 + (s == j.share0)) * p.T * 128; };
     float* mine = part(j.share);
@@ -728,7 +801,7 @@ __device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mas
     bar_epilogue();
     if (c.tid == 0) {
         uint32_t* ctr = p.ctr + CTR_TILE + j.share0;
-        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(j.share1 - j.share0);
+        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(parts - 1);
         if (last) *ctr = 0;
         __threadfence();
         *last_s = last;
@@ -743,8 +816,9 @@ __device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mas
     for (int i = c.tid; i < p.T * 32; i += EPI) {
         if (!(mask >> (i / 32) & 1u)) continue;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int s = j.share0; s <= j.share1; ++s) {
+#pragma unroll 8
+        for (int x = 0; x < parts; ++x) {
+            const int s = j.share0 + x <= j.share1 ? j.share0 + x : j.small0 + x - (j.share1 - j.share0 + 1);
             const float4 w = __ldcg(reinterpret_cast<const float4*>(part(s)) + i);
             v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
         }
@@ -1073,14 +1147,12 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
 #pragma unroll 1
                 while (ok && plan.next(j)) {
                     const void* sc = third ? (j.shared ? p.ws2s : p.w2s) : (j.shared ? p.ws1s : p.w1s);
-                    ok = post<MODE>(c, queue, j, static_cast<const float*>(sc)) &&
-                         load_weights<MODE>(c, j, third ? (j.shared ? &p.ws2 : &p.w2) : (j.shared ? &p.ws1 : &p.w1),
-                                            static_cast<const uint8_t*>(sc), ring);
+                    ok = load_job<MODE>(c, queue, j, third ? (j.shared ? &p.ws2 : &p.w2) : (j.shared ? &p.ws1 : &p.w1), sc,
+                                        ring);
                 }
                 share = __shfl_sync(0xffffffffu, after, 0);
             }
-            j.p0 = -1;
-            ok = ok && post<MODE>(c, queue, j, nullptr);
+            ok = ok && end_phase(c, queue);
         }
         // a block that gave up leaves its copies the time to land before it
         // gives its memory back (their barriers may never complete)
