@@ -324,19 +324,20 @@ def moe_layer_forward_few(cfg, x, W_r, logit_bias, W1, W1_scales, b1, W2, W2_sca
 def _mxfp4_args(dense, codes, scales, what: str):
     """(dtype, rows, cols) of a dense matrix and its MXFP4 form, checked against each other."""
     import torch
-    dtypes = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-    if dense.dtype not in dtypes:
+    dt = dense.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
         raise ValueError(f"{what}: the dense matrix must be float32 or bfloat16")
-    if dense.dim() < 1 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if dense.dim() < 1 or codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError(f"{what}: codes and scales are uint8 matrices")
-    cols = dense.shape[-1]
+    cols, n = dense.shape[-1], dense.numel()
     if cols < 1 or cols % 32:
         raise ValueError(f"{what}: the last dimension ({cols}) must be a multiple of 32")
-    if codes.numel() * 2 != dense.numel() or scales.numel() * 32 != dense.numel():
+    if codes.numel() * 2 != n or scales.numel() * 32 != n:
         raise ValueError(f"{what}: codes need (..., cols / 2) and scales (..., cols / 32) elements")
-    if not dense.device == codes.device == scales.device:
+    dev = dense.device
+    if dev != codes.device or dev != scales.device:
         raise ValueError(f"{what}: all tensors must be on one device")
-    return dtypes[dense.dtype], dense.numel() // cols, cols
+    return MOE_F32 if dt is torch.float32 else MOE_BF16, n // cols, cols
 
 
 def moe_mxfp4_quantize(x, codes, scales, stream=None):
@@ -394,6 +395,10 @@ def moe_mxfp4_matmul(shape, a, a_scales, seg_offsets, seg_mat, w, w_scales, bias
            "moe_mxfp4_matmul")
 
 
+_FEW_WEIGHTS = ("W_r", "logit_bias", "W1", "W1_scales", "b1", "W2", "W2_scales", "b2",
+                "Ws1", "Ws1_scales", "bs1", "Ws2", "Ws2_scales", "bs2")
+
+
 class MoELayer:
     """A layer shape plus device-resident weights and workspace.
 
@@ -421,6 +426,8 @@ class MoELayer:
             self.ws = torch.empty(moe_workspace_size(cfg), dtype=torch.uint8, device=self.device)
             moe_workspace_init(cfg, self.ws)
         self._few_ws = self.ws if cfg.dtype == MOE_MXFP4 else None
+        self._few_known = None                                 # the tensors whose layout forward_few has checked
+        self._cfg_ref = ctypes.byref(cfg)
         out_dt = torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16
         self.out = torch.empty((cfg.T, cfg.d_model), dtype=out_dt, device=self.device)
         self.f = torch.empty(cfg.n_routed, dtype=torch.float32, device=self.device)
@@ -451,11 +458,15 @@ class MoELayer:
         if self._few_ws is None:
             self._few_ws = self._few_workspace()
         w = self.w
-        g = lambda k: w.get(k)  # noqa: E731
-        moe_layer_forward_few(self.cfg, x, g("W_r"), g("logit_bias"), g("W1"), g("W1_scales"), g("b1"),
-                              g("W2"), g("W2_scales"), g("b2"), g("Ws1"), g("Ws1_scales"), g("bs1"),
-                              g("Ws2"), g("Ws2_scales"), g("bs2"), self.out, self.f, self.P, self.loss,
-                              self.topk_idx, self.gates, self.counts, self._few_ws, stream)
+        tensors = [w.get(k) for k in _FEW_WEIGHTS]
+        tensors += (self.out, self.f, self.P, self.loss, self.topk_idx, self.gates, self.counts, self._few_ws)
+        known = self._few_known
+        if known is None or any(a is not b for a, b in zip(known, tensors)):
+            for t in tensors:
+                _p(t)                                          # on the GPU, dense
+            self._few_known = tensors
+        ptrs = [None if t is None else t.data_ptr() for t in tensors]
+        _check(lib().moe_layer_forward_few(self._cfg_ref, _p(x), *ptrs, _stream(stream)), "moe_layer_forward_few")
         return self.out, self.f, self.P, self.loss
 
     def _forward_into(self, x, out, loss, stream=None):

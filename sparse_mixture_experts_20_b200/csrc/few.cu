@@ -174,6 +174,13 @@ template <int MODE> __host__ __device__ constexpr int pieces_of(int k) { return 
 
 __device__ __forceinline__ void bar_general() { asm volatile("bar.sync 1, %0;" :: "n"(CT) : "memory"); }
 __device__ __forceinline__ void bar_epilogue() { asm volatile("bar.sync 2, %0;" :: "n"(EPI) : "memory"); }
+// The epilogue warps agree: true if every one of them is ok.
+__device__ __forceinline__ bool all_ok(bool ok) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.red.and.pred q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(ok)), "n"(EPI) : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void bar_upper() { asm volatile("bar.sync 3, %0;" :: "n"(EPI) : "memory"); }       // warps 4..7
 // The general warps and the token loader: what phase 2 or 3 reads is in memory.
 __device__ __forceinline__ void bar_tokens_ready() { asm volatile("bar.sync 4, %0;" :: "n"(CT + 32) : "memory"); }
@@ -621,12 +628,6 @@ struct MmaState {
     bool leader;
     uint32_t tags = 0x100u;      // FP8, lane i: the exponent whose uniform scales are in set i
 };
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 
 // FP8: the columns with the weight scale 2^(e - 127) for every row.  A set is
 // rewritten when another exponent of the same residue comes up, once the MMAs
@@ -1256,21 +1257,29 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
             }
             bool begins = true;
             Job j;
-            while (queue.next(c, j, ok)) {
-                queue.done(c);
-                if (begins) {
-#pragma unroll 1
-                    for (int t = 0; t < p.T; ++t) sums[t * 128] = 0.f;
-                }
-                begins = j.ends;
+            while (true) {
+                const bool got = queue.next(c, j, ok);
                 const int row = j.row0 + c.tid;
-                const bool in = row < j.n;
-                // phase 3: the share with a matrix's first piece adds its bias
-                const float* biases = third ? (j.shared ? p.bs2 : p.b2) : (j.shared ? p.bs1 : p.b1);
-                const float bias = in && (!third || j.p0 == 0) ? __ldg(biases + static_cast<size_t>(j.mat) * j.n + row) : 0.f;
-                read_job<MODE>(c, j, third, third ? bias : 0.f, tmem, accf, acce, jobs_read, ok, sums);
+                const bool in = got && row < j.n;
+                float bias = 0.f;
+                if (got) {
+                    queue.done(c);
+                    if (begins) {
+#pragma unroll 1
+                        for (int t = 0; t < p.T; ++t) sums[t * 128] = 0.f;
+                    }
+                    begins = j.ends;
+                    // phase 3: the share with a matrix's first piece adds its bias
+                    const float* biases = third ? (j.shared ? p.bs2 : p.b2) : (j.shared ? p.bs1 : p.b1);
+                    if (in && (!third || j.p0 == 0)) bias = __ldg(biases + static_cast<size_t>(j.mat) * j.n + row);
+                    read_job<MODE>(c, j, third, third ? bias : 0.f, tmem, accf, acce, jobs_read, ok, sums);
+                }
+                // a wait that gave up ends the phase for the four warps together:
+                // what follows has barriers between them
+                ok = all_ok(ok);
+                if (!ok || !got) break;
                 const uint32_t tokens = third ? (1u << p.T) - 1u : j.mask;
-                if (!j.ends || !combine(c, j, tokens, out_s) || !in || !ok) continue;
+                if (!j.ends || !combine(c, j, tokens, out_s) || !in) continue;
 #pragma unroll 1
                 for (uint32_t m = tokens; m; m &= m - 1) {
                     const int t = __ffs(m) - 1;

@@ -17,14 +17,20 @@
 //               and B 32 KB;
 //   warp 1      MMA issuer: per stage copies the scales from shared to tensor
 //               memory (tcgen05.cp 32x128b.warpx4, in order with the MMAs),
-//               then 4 MMAs of K = 64;
+//               then 4 MMAs of K = 64.  The warp runs the loop as a whole and
+//               one elected lane issues, so that descriptors are warp-uniform
+//               (a loop that one lane runs alone took 2600 cycles a stage);
 //   warps 2..5  epilogue: bias, SiLU, and bf16, fp32 or MXFP4 rows (a chunk
-//               of 32 columns per tcgen05.ld is one block of the output);
+//               of 32 columns per tcgen05.ld is one block of the output),
+//               which leave through shared memory, 64 bytes of a row at a time,
+//               so that a store instruction writes whole sectors of 8 rows (a
+//               row a lane, 16 bytes at a time, cost a third of the kernel);
 //   warps 6..9  scale loaders: a thread reads the 8 scale bytes of its A row
-//               and of two weight rows for a stage and lays them out in shared
-//               memory as tcgen05.cp reads them: 512 bytes per 128 rows and
-//               128 elements of K, row r's four bytes at
-//               16 (r mod 32) + 4 (r div 32).
+//               and of two weight rows for a stage (LOOKAHEAD stages early)
+//               and lays them out in shared memory as tcgen05.cp reads them:
+//               512 bytes per 128 rows and 128 elements of K, row r's four
+//               bytes at 16 (r mod 32) + 4 (r div 32).  The MMA warp, which has
+//               nothing else in flight, makes the proxy fence.
 // Every wait is bounded (common.cuh).
 #include "ffn_common.cuh"
 #include "mxfp4.cuh"
@@ -39,7 +45,7 @@ constexpr int BN = 256, BKB = 128;                   // weight rows per tile; by
 constexpr int STAGES = 4;
 constexpr uint32_t TMEM_COLS = 512, ACC1_COL = 192, SF_COL0 = 448, SF_STRIDE = 24;
 constexpr uint32_t FULL_ARRIVALS = 1 + 4;            // TMA expect_tx + one lane per loader warp
-constexpr int LOOKAHEAD = 2;                         // stages of scales a loader has in flight in registers
+constexpr int LOOKAHEAD = 4;                         // stages of scales a loader has in flight in registers
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 constexpr uint64_t kDrainTimeoutNs = 200000000ull;
 
@@ -52,8 +58,9 @@ constexpr int OFF_BAR = OFF_SF + STAGES * SF_BYTES;
 constexpr int N_BARS = 2 * STAGES + 4 + 2;           // full, empty [STAGES]; accf, acce [2]; ovl; drain
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int OFF_SEG = OFF_MISC + 16;
-constexpr int OFF_BIAS = (OFF_SEG + SegTable::SEG_INTS * 4 + 15) & ~15;   // per epilogue warp, 2 x BN fp32
-constexpr int TOTAL = OFF_BIAS + 4 * 2 * BN * 4;
+constexpr int OFF_BIAS = (OFF_SEG + SegTable::SEG_INTS * 4 + 15) & ~15;   // 2 x BN fp32, the tiles in flight
+constexpr int OFF_OUT = (OFF_BIAS + 2 * BN * 4 + 127) & ~127;             // per epilogue warp, 32 rows x 64 bytes of output
+constexpr int TOTAL = OFF_OUT + 4 * 32 * 64;
 constexpr int ALLOC = TOTAL + 1024;
 static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 static_assert(OFF_SF % 128 == 0 && OFF_BAR % 8 == 0, "alignment");
@@ -161,39 +168,43 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA issuer
-        if (lane == 0) {
-            int stage = 0, abuf = 0;
-            uint32_t phase = 0, aph0 = 0, aph1 = 0, ovl_ph = 0;
-            long long item = 0;
-            bool ok = true, issued_any = false, first = true;
-            for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
-                // the previous tile's overlapping columns drained, and this
-                // buffer's tile from two tiles back fully drained
-                if (!first) {
-                    if (!mbar_wait_bounded(ovl, ovl_ph, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
-                    ovl_ph ^= 1u;
+        const bool leader = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+            return __all_sync(0xffffffffu, mma_wait_spin(bar, parity, abort_flag, p.status, p.timeout_ns)) != 0;
+        };
+        int stage = 0, abuf = 0, item = 0;
+        uint32_t phase = 0, aph0 = 0, aph1 = 0, ovl_ph = 0;
+        bool ok = true, first = true;
+#pragma unroll 1
+        for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
+            // the previous tile's overlapping columns drained, and this
+            // buffer's tile from two tiles back fully drained
+            if (!first) {
+                if (!wait(ovl, ovl_ph)) { ok = false; break; }
+                ovl_ph ^= 1u;
+            }
+            first = false;
+            uint32_t& aph = abuf ? aph1 : aph0;
+            if (!wait(&acce[abuf], aph ^ 1u)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (abuf ? ACC1_COL : 0u);
+#pragma unroll 1
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!wait(&full[stage], phase)) { ok = false; break; }
+                fence_proxy_async_smem();
+                // the MMAs that read this scale slot two stages ago are done
+                if (item >= 2) {
+                    const int s2 = (stage + STAGES - 2) % STAGES;
+                    if (!wait(&empty[s2], stage >= 2 ? phase : phase ^ 1u)) { ok = false; break; }
                 }
-                first = false;
-                uint32_t& aph = abuf ? aph1 : aph0;
-                if (!mbar_wait_bounded(&acce[abuf], aph ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                item = item < 2 ? item + 1 : 2;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (abuf ? ACC1_COL : 0u);
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_try_wait(&full[stage], phase) &&
-                        !mma_wait_spin(&full[stage], phase, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
-                    // the MMAs that read this scale slot two stages ago are done
-                    if (item >= 2) {
-                        const int s2 = (stage + STAGES - 2) % STAGES;
-                        const uint32_t ph2 = stage >= 2 ? phase : phase ^ 1u;
-                        if (!mbar_try_wait(&empty[s2], ph2) &&
-                            !mma_wait_spin(&empty[s2], ph2, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
-                    }
-                    ++item;
-                    tc_fence_after();
-                    const uint64_t adesc = smem_desc_k_sw128(smem + OFF_A + stage * A_BYTES);
-                    const uint64_t bdesc = smem_desc_k_sw128(smem + OFF_B + stage * B_BYTES);
-                    const uint8_t* sf = smem + OFF_SF + stage * SF_BYTES;
-                    const uint32_t slot = tmem_base + SF_COL0 + static_cast<uint32_t>(stage & 1) * SF_STRIDE;
+                const uint64_t adesc = smem_desc_k_sw128(smem + OFF_A + stage * A_BYTES);
+                const uint64_t bdesc = smem_desc_k_sw128(smem + OFF_B + stage * B_BYTES);
+                const uint8_t* sf = smem + OFF_SF + stage * SF_BYTES;
+                const uint32_t slot = tmem_base + SF_COL0 + static_cast<uint32_t>(stage & 1) * SF_STRIDE;
+                if (leader) {
 #pragma unroll
                     for (int j = 0; j < 6; ++j) tmem_cp_scales(slot + 4 * j, sf + 512 * j);
 #pragma unroll
@@ -202,48 +213,72 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
                         umma_mxf4_bs(d_tmem, adesc + 2 * k, bdesc + 2 * k, make_idesc_mxf4(BN, 2 * (k & 1)), s, s + 4,
                                      (kb > 0 || k > 0) ? 1u : 0u);
                     }
-                    issued_any = true;
                     umma_commit(&empty[stage]);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
-                if (!ok) break;
-                umma_commit(&accf[abuf]);
-                aph ^= 1u;
-                abuf ^= 1;
+                __syncwarp();
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
-            if (!ok && issued_any) {
-                umma_commit(drain);
-                volatile int no_abort = 0;
-                mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainTimeoutNs);
-            }
+            if (!ok) break;
+            if (leader) umma_commit(&accf[abuf]);
+            __syncwarp();
+            aph ^= 1u;
+            abuf ^= 1;
+        }
+        if (!ok && leader) {
+            umma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainTimeoutNs);
         }
         __syncwarp();
     } else if (warp < 6) {
         // ================= epilogue (warps 2..5)
         const int quad = warp & 3;
-        const int r_local = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         int abuf = 0;
         uint32_t fph0 = 0, fph1 = 0;
+        bool ok = true;
         for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x) {
             const TileInfo ti = decode_tile<BN, 2 * BKB>(tile, p, seg, nseg);
             const GroupDev& g = p.g[0];
-            const bool row_ok = r_local < ti.rows_left;
-            float* bias_s = reinterpret_cast<float*>(smem + OFF_BIAS) + (quad * 2 + abuf) * BN;
-#pragma unroll
-            for (int i = 4 * lane; i < BN; i += 128) {
+            // the tile's biases, a quarter from each warp; the buffer's tile from
+            // two tiles back is done with in every warp, which all were here
+            // for the tile between
+            float* bias_s = reinterpret_cast<float*>(smem + OFF_BIAS) + abuf * BN;
+            if (lane < 16) {
+                const int i = quad * 64 + 4 * lane;
                 const float4 v = (g.bias && ti.n0 + i < N)
                     ? __ldg(reinterpret_cast<const float4*>(g.bias + static_cast<size_t>(ti.mat) * N + ti.n0 + i))
                     : make_float4(0.f, 0.f, 0.f, 0.f);
                 *reinterpret_cast<float4*>(bias_s + i) = v;
             }
-            __syncwarp();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
             uint32_t& fph = abuf ? fph1 : fph0;
-            if (!warp_wait(&accf[abuf], fph, abort_flag, p.status, p.timeout_ns, lane)) break;
+            // (after a wait gave up the warps keep meeting at the barrier above)
+            if (ok) ok = warp_wait(&accf[abuf], fph, abort_flag, p.status, p.timeout_ns, lane);
+            if (!ok) { abuf ^= 1; continue; }
             fph ^= 1u;
             tc_fence_after();
             const uint32_t acc = lane_base + (abuf ? ACC1_COL : 0u);
-            const size_t row = static_cast<size_t>(ti.c_row + r_local);
+            const size_t row0 = static_cast<size_t>(ti.c_row + quad * 32);       // the warp's first row
+            const int rows = min(32, ti.rows_left - quad * 32);                  // of them valid (may be negative)
+            uint8_t* stage = smem + OFF_OUT + quad * 32 * 64;
+            // 16-byte chunk q of row r of the staging is at q ^ ((r >> 1) & 3),
+            // which spreads the lanes' writes and reads over the banks
+            auto put = [&](int q, const uint4& v) {
+                *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = v;
+            };
+            // the warp's rows, 64 bytes each, to byte `at` of rows of `pitch` bytes; only `bytes` of them
+            auto flush = [&](size_t pitch, size_t at, int bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int r8 = 0; r8 < 32; r8 += 8) {
+                    const int r = r8 + (lane >> 2), q = lane & 3;
+                    if (r < rows && 16 * q < bytes)
+                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + (row0 + r) * pitch + at + 16 * q) =
+                            *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+                }
+                __syncwarp();
+            };
             // chunks of 32 columns, the overlapping ones (6, 7 of buffer 0;
             // 0, 1 of buffer 1) first
 #pragma unroll 1
@@ -255,7 +290,7 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
                 if (ci == 1) { tc_fence_before(); mbar_arrive(ovl); }
                 else if (ci == BN / 32 - 1) { tc_fence_before(); mbar_arrive(&acce[abuf]); }
                 const int n = ti.n0 + c * 32;
-                if (!row_ok || n >= N) continue;
+                if (rows <= 0 || n >= N) continue;               // (the same for the whole warp)
                 float v[32];
                 const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
 #pragma unroll
@@ -271,11 +306,17 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
                     for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
                 }
                 if constexpr (OUT == MOE_F32) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(g.C) + row * N + n);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float* f = v + 16 * h + 4 * q;
+                            put(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                              __float_as_uint(f[3])));
+                        }
+                        flush(4 * static_cast<size_t>(N), 4 * static_cast<size_t>(n + 16 * h), 64);
+                    }
                 } else if constexpr (OUT == MOE_BF16) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.C) + row * N + n);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t w[4];
@@ -284,8 +325,9 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
                             __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * q + 2 * h], v[8 * q + 2 * h + 1]);
                             w[h] = *reinterpret_cast<uint32_t*>(&t);
                         }
-                        dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                        put(q, make_uint4(w[0], w[1], w[2], w[3]));
                     }
+                    flush(2 * static_cast<size_t>(N), 2 * static_cast<size_t>(n), 64);
                 } else {
                     uint32_t m = 0;
 #pragma unroll
@@ -300,9 +342,12 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
                         for (int j = 0; j < 8; ++j) t[j] = v[8 * q + j] * inv;
                         w[q] = sb == 255u ? 0u : f32x8_to_e2m1x8(t);
                     }
-                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + (row * N + n) / 2) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
-                    mp.y_scales[(row * N + n) / 32] = static_cast<uint8_t>(sb);
+                    // chunks come in runs of 4 (6 7 0 1 | 2 3 4 5, or 0 1 2 3 | 4 5 6 7) of
+                    // which two neighbours make 32 bytes of a row: one sector
+                    put(c & 1, make_uint4(w[0], w[1], w[2], w[3]));
+                    if (lane < rows) mp.y_scales[((row0 + lane) * N + n) / 32] = static_cast<uint8_t>(sb);
+                    if ((c & 1) || n + 32 >= N)
+                        flush(static_cast<size_t>(N) / 2, (static_cast<size_t>(n) - (c & 1) * 32) / 2, 16 * ((c & 1) + 1));
                 }
             }
             abuf ^= 1;
@@ -329,6 +374,12 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
             const int k0 = it.kb * 8;
             const bool two = k0 + 4 < kq;
             auto row = [&](const uint8_t* base, bool ok, uint32_t& lo, uint32_t& hi) {
+                if (kq % 8 == 0) {                           // both words of the stage at once
+                    const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(base + k0)) : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    lo = v.x;
+                    hi = v.y;
+                    return;
+                }
                 lo = ok ? __ldg(reinterpret_cast<const uint32_t*>(base + k0)) : 0x7F7F7F7Fu;
                 hi = ok && two ? __ldg(reinterpret_cast<const uint32_t*>(base + k0 + 4)) : 0x7F7F7F7Fu;
             };
@@ -340,31 +391,64 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
         Item cur, ahead;
         start(cur);
         start(ahead);
-        uint32_t ring[LOOKAHEAD][6];
-#pragma unroll
-        for (int j = 0; j < LOOKAHEAD; ++j)
-            if (ahead.tile < total_tiles) { load(ahead, ring[j]); advance(ahead); }
         int stage = 0;
         uint32_t phase = 0;
         bool aborted = false;
+        auto store = [&](const uint32_t (&v)[6]) {
+            if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.timeout_ns, lane)) { aborted = true; return; }
+            uint32_t* dst = dst0 + stage * (SF_BYTES / 4);
+#pragma unroll
+            for (int q = 0; q < 6; ++q) dst[q * 128] = v[q];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[stage]);
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            advance(cur);
+        };
+        if (kq % 16 == 0) {
+            // K a multiple of 512: the words of two stages are one 16-byte read
+            // (the scattered reads are what the loaders spend their time on)
+            auto load2 = [&](const Item& it, uint4 (&v)[3]) {
+                const uint4 one = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                auto row = [&](const uint8_t* base, bool ok) {
+                    return ok ? __ldg(reinterpret_cast<const uint4*>(base + it.kb * 8)) : one;
+                };
+                v[0] = row(mp.a_scales + static_cast<size_t>(it.ti.a_row + i) * kq, i < it.ti.rows_left);
+                const uint8_t* w = mp.w_scales + (static_cast<size_t>(it.ti.mat) * N + it.ti.n0 + i) * kq;
+                v[1] = row(w, it.ti.n0 + i < N);
+                v[2] = row(w + static_cast<size_t>(128) * kq, it.ti.n0 + 128 + i < N);
+            };
+            constexpr int PAIRS = LOOKAHEAD / 2;
+            uint4 ring[PAIRS][3];
+            auto fetch = [&](uint4 (&v)[3]) {
+                if (ahead.tile < total_tiles) { load2(ahead, v); advance(ahead); advance(ahead); }
+            };
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) fetch(ring[j]);
 #pragma unroll 1
-        while (cur.tile < total_tiles && !aborted) {
+            while (cur.tile < total_tiles && !aborted) {
 #pragma unroll
-            for (int j = 0; j < LOOKAHEAD; ++j) {
-                if (cur.tile >= total_tiles) break;
-                if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.timeout_ns, lane)) {
-                    aborted = true;
-                    break;
+                for (int j = 0; j < PAIRS; ++j) {
+                    if (cur.tile >= total_tiles || aborted) break;
+                    const uint4* v = ring[j];
+                    store({v[0].x, v[1].x, v[2].x, v[0].y, v[1].y, v[2].y});
+                    if (aborted) break;
+                    store({v[0].z, v[1].z, v[2].z, v[0].w, v[1].w, v[2].w});
+                    fetch(ring[j]);
                 }
-                uint32_t* dst = dst0 + stage * (SF_BYTES / 4);
+            }
+        } else {
+            uint32_t ring[LOOKAHEAD][6];
 #pragma unroll
-                for (int q = 0; q < 6; ++q) dst[q * 128] = ring[j][q];
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[stage]);
+            for (int j = 0; j < LOOKAHEAD; ++j)
                 if (ahead.tile < total_tiles) { load(ahead, ring[j]); advance(ahead); }
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                advance(cur);
+#pragma unroll 1
+            while (cur.tile < total_tiles && !aborted) {
+#pragma unroll
+                for (int j = 0; j < LOOKAHEAD; ++j) {
+                    if (cur.tile >= total_tiles || aborted) break;
+                    store(ring[j]);
+                    if (ahead.tile < total_tiles) { load(ahead, ring[j]); advance(ahead); }
+                }
             }
         }
     }
