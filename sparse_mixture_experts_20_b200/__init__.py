@@ -170,8 +170,17 @@ def _p(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():                        # the same handle, without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
+
+
+def _on_current_device(t, what: str):
+    """The library launches on the current device and its stream: a tensor of another one is refused."""
+    import torch
+    if t.is_cuda and t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: the tensors are on {t.device}, which is not the current device")
 
 
 def _check(status: int, where: str):
@@ -343,6 +352,7 @@ def _mxfp4_args(dense, codes, scales, what: str):
 def moe_mxfp4_quantize(x, codes, scales, stream=None):
     """x (..., cols) float32 / bfloat16 into MXFP4: codes uint8 (..., cols / 2), scales uint8 (..., cols / 32)."""
     dtype, rows, cols = _mxfp4_args(x, codes, scales, "moe_mxfp4_quantize")
+    _on_current_device(x, "moe_mxfp4_quantize")
     _check(lib().moe_mxfp4_quantize(_p(x), dtype, rows, cols, _p(codes), _p(scales), _stream(stream)),
            "moe_mxfp4_quantize")
 
@@ -350,6 +360,7 @@ def moe_mxfp4_quantize(x, codes, scales, stream=None):
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """The values of an MXFP4 matrix into out (..., cols) float32 / bfloat16."""
     dtype, rows, cols = _mxfp4_args(out, codes, scales, "moe_mxfp4_dequantize")
+    _on_current_device(out, "moe_mxfp4_dequantize")
     _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _p(out), dtype, _stream(stream)),
            "moe_mxfp4_dequantize")
 
@@ -360,6 +371,7 @@ def moe_mxfp4_tile_scales(scales, stream=None):
     import torch
     if scales.dim() != 3 or scales.dtype != torch.uint8 or scales.shape[1] < 1 or scales.shape[2] < 1:
         raise ValueError("moe_mxfp4_tile_scales: scales are a uint8 stack (n_mats, rows, cols / 32)")
+    _on_current_device(scales, "moe_mxfp4_tile_scales")
     n, rows, cols = scales.shape[0], scales.shape[1], scales.shape[2] * 32
     tiled = torch.empty((n, (rows + 127) // 128, cols // 128, 512), dtype=torch.uint8, device=scales.device)
     _check(lib().moe_mxfp4_tile_scales(_p(scales), n, rows, cols, _p(tiled), _stream(stream)), "moe_mxfp4_tile_scales")
@@ -390,6 +402,17 @@ def moe_mxfp4_get_device_status(shape, ws, stream=None, clear: bool = False) -> 
 
 def moe_mxfp4_matmul(shape, a, a_scales, seg_offsets, seg_mat, w, w_scales, bias, y, y_scales, ws, stream=None):
     """y[r] = act(W_e a[r] + bias_e) over segments of rows, both operands in MXFP4 (shape: make_mxfp4_shape)."""
+    s = shape
+    wb = s.n_mats * s.n * s.k
+    bits = {MOE_F32: 32, MOE_BF16: 16, MOE_MXFP4: 4}.get(s.out_dtype, 0)
+    for name, t, nbytes in (("a", a, s.rows * s.k // 2), ("a_scales", a_scales, s.rows * s.k // 32),
+                            ("seg_offsets", seg_offsets, 4 * (s.n_seg + 1)), ("seg_mat", seg_mat, 4 * s.n_seg),
+                            ("w", w, wb // 2), ("w_scales", w_scales, wb // 32), ("bias", bias, 4 * s.n_mats * s.n),
+                            ("y", y, s.rows * s.n * bits // 8), ("y_scales", y_scales, s.rows * s.n // 32)):
+        if t is not None and t.numel() * t.element_size() < nbytes:
+            raise ValueError(f"moe_mxfp4_matmul: {name} is smaller than its shape says")
+    if y is not None:
+        _on_current_device(y, "moe_mxfp4_matmul")
     _check(lib().moe_mxfp4_matmul(ctypes.byref(shape), _p(a), _p(a_scales), _p(seg_offsets), _p(seg_mat), _p(w),
                                   _p(w_scales), _p(bias), _p(y), _p(y_scales), _p(ws), _stream(stream)),
            "moe_mxfp4_matmul")
@@ -465,6 +488,9 @@ class MoELayer:
             for t in tensors:
                 _p(t)                                          # on the GPU, dense
             self._few_known = tensors
+        if x.dtype != self.out.dtype or x.numel() != self.out.numel():
+            raise ValueError("forward_few: x must be bfloat16 (T, d_model)")
+        _on_current_device(x, "forward_few")
         ptrs = [None if t is None else t.data_ptr() for t in tensors]
         _check(lib().moe_layer_forward_few(self._cfg_ref, _p(x), *ptrs, _stream(stream)), "moe_layer_forward_few")
         return self.out, self.f, self.P, self.loss

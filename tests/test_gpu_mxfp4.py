@@ -202,3 +202,112 @@ def test_nan_block_reaches_its_row_only():
                        torch.zeros(1, dtype=torch.int32, device="cuda"), wc, wsc, None, y, None, ws)
     bad = torch.isnan(y).any(1).nonzero().flatten().tolist()
     assert bad == [5, 129] and bool(torch.isnan(y[[5, 129]]).all())
+
+
+@pytest.mark.parametrize("n,rows,cols", [(1, 1, 128), (3, 130, 256), (2, 256, 1408)])
+def test_tile_scales(n, rows, cols):
+    s = torch.randint(0, 256, (n, rows, cols // 32), dtype=torch.uint8, generator=torch.Generator().manual_seed(rows))
+    got = M.moe_mxfp4_tile_scales(s.cuda()).cpu().numpy()
+    tiles = (rows + 127) // 128
+    assert got.shape == (n, tiles, cols // 128, 512)
+    for m in range(n):
+        for r in range(128 * tiles):
+            at = 16 * (r % 32) + 4 * (r % 128 // 32)
+            words = got[m, r // 128, :, at:at + 4].ravel()
+            assert np.array_equal(words, s[m, r].numpy() if r < rows else np.full(cols // 32, 127))
+
+
+def test_matmul_repeats_bit_for_bit_captured_and_on_a_side_stream():
+    k, n, rows = 640, 352, 333
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    (ac, asc), (wc, wsc) = (quantize(torch.randn(r, k, device="cuda", generator=gen)) for r in (rows, 2 * n))
+    offs = torch.tensor([0, 200, rows], dtype=torch.int32, device="cuda")
+    mats = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    s = M.make_mxfp4_shape(rows, n, k, 2, 2, M.MOE_ACT_SILU, M.MOE_BF16)
+    ws = torch.zeros(M.moe_mxfp4_workspace_size(s), dtype=torch.uint8, device="cuda")
+    y = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+
+    def call():
+        M.moe_mxfp4_matmul(s, ac, asc, offs, mats, wc, wsc, None, y, None, ws)
+
+    call()
+    first = y.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(5):
+            y.zero_()
+            call()
+        assert torch.equal(y, first)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+        assert torch.equal(y, first)
+
+
+@pytest.mark.parametrize("seed,T,d,E,K,dff", [(0, 70, 256, 8, 2, 384), (1, 300, 640, 5, 3, 128)])
+def test_experts_of_a_layer_in_four_bits(seed, T, d, E, K, dff):
+    """Route, dispatch, quantise, two products (the hidden activation in MXFP4 between them) and combine, as a
+    prompt goes through; then the first tokens through the few-token layer with the same weights."""
+    from synthetic import MoEShape, make_inputs
+    sh = MoEShape("four bits", T, d, E, K, dff, dtype=M.MOE_BF16)
+    inp = make_inputs(sh, seed)
+    w = {}
+    for name in ("W1", "W2"):
+        m = inp[name].double().numpy()
+        codes, scales = O.mxfp4_encode(m.reshape(-1, m.shape[-1]))
+        w[name] = O.mxfp4_decode(codes, scales).reshape(m.shape)
+        inp[name] = torch.tensor(codes).reshape(*m.shape[:2], -1)
+        inp[name + "_scales"] = torch.tensor(scales).reshape(*m.shape[:2], -1)
+    g = {k: None if v is None else v.cuda() for k, v in inp.items()}
+    cfg = M.make_config(sh)
+    cap, r_cap, x_rows, _ = M.moe_buffer_rows(cfg)
+    i32, f32, u8 = (dict(dtype=t, device="cuda") for t in (torch.int32, torch.float32, torch.uint8))
+    ws = torch.empty(M.moe_workspace_size(cfg), **u8)
+    M.moe_workspace_init(cfg, ws)
+    idx, gates = torch.empty((T, K), **i32), torch.empty((T, K), **f32)
+    counts, kept, offs = torch.empty(E, **i32), torch.empty(E, **i32), torch.empty(E + 1, **i32)
+    slot_row, row_slot = torch.empty((T, K), **i32), torch.empty(r_cap, **i32)
+    xd = torch.empty((x_rows, d), dtype=torch.bfloat16, device="cuda")
+    M.moe_route(cfg, g["x"], g["W_r"], None, idx, gates, None, ws)
+    M.moe_dispatch(cfg, g["x"], idx, counts, kept, offs, slot_row, row_slot, xd, None, ws)
+    a, asc = quantize(xd)
+    mats = torch.arange(E, **i32)
+    s1 = M.make_mxfp4_shape(r_cap, dff, d, E, E, M.MOE_ACT_SILU, M.MOE_MXFP4)
+    s2 = M.make_mxfp4_shape(r_cap, d, dff, E, E, M.MOE_ACT_NONE, M.MOE_BF16)
+    mws = torch.empty(M.moe_mxfp4_workspace_size(s1), **u8)
+    M.moe_mxfp4_workspace_init(s1, mws)
+    h, hsc = torch.empty((r_cap, dff // 2), **u8), torch.empty((r_cap, dff // 32), **u8)
+    y = torch.empty((r_cap, d), dtype=torch.bfloat16, device="cuda")
+    M.moe_mxfp4_matmul(s1, a, asc, offs, mats, g["W1"], g["W1_scales"], g["b1"], h, hsc, mws)
+    M.moe_mxfp4_matmul(s2, h, hsc, offs, mats, g["W2"], g["W2_scales"], g["b2"], y, None, mws)
+    out = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    M.moe_combine(cfg, y, gates, slot_row, out)
+    assert M.moe_get_device_status(cfg, ws) == 0 and M.moe_mxfp4_get_device_status(s1, mws) == 0
+
+    x = inp["x"].double().numpy()
+    idx_h, gates_h = idx.cpu().numpy(), gates.double().cpu().numpy()
+    xq = O.mxfp4_decode(*O.mxfp4_encode(x))
+    four, exact = np.zeros((T, d)), np.zeros((T, d))
+    for t in range(T):
+        for k in range(K):
+            e = idx_h[t, k]
+            b1, b2 = inp["b1"][e].double().numpy(), inp["b2"][e].double().numpy()
+            silu = lambda z: z / (1 + np.exp(-z))  # noqa: E731
+            hq = O.mxfp4_decode(*O.mxfp4_encode(silu(w["W1"][e] @ xq[t] + b1)[None]))[0]
+            four[t] += gates_h[t, k] * (w["W2"][e] @ hq + b2)
+            exact[t] += gates_h[t, k] * (w["W2"][e] @ silu(w["W1"][e] @ x[t] + b1) + b2)
+    rel = lambda u, v: np.linalg.norm(u - v) / np.linalg.norm(v)  # noqa: E731
+    # y and out rounded to bf16 (2^-8 at most, each on average less than half of it), and an h within fp32's error
+    # of a border (one in some 10^4) rounded to its other side, a quarter of itself away: 0.25 / 100 of the norm
+    assert rel(out.double().cpu().numpy(), four) < 2.0 ** -8 + 0.0025
+
+    n = 5
+    few = M.MoELayer(M.make_config(sh, T=n, dtype=M.MOE_MXFP4), g)
+    got = few.forward_few(g["x"][:n])[0].double().cpu().numpy()
+    assert np.array_equal(few.topk_idx.cpu().numpy(), idx_h[:n])
+    assert rel(got, exact[:n]) < 2.0 ** -8

@@ -120,3 +120,35 @@ def test_layer_entry_points_reject_mxfp4():
     cfg = M.make_config(T=4, d_model=128, n_routed=8, top_k=2, d_ff=128, dtype=M.MOE_MXFP4)
     n = ctypes.c_size_t(0)
     assert M.lib().moe_workspace_size(ctypes.byref(cfg), ctypes.byref(n)) == M.MOE_ERR_INVALID_ARG
+
+
+def test_tile_scales_refusals():
+    n0 = M.moe_kernel_launches()
+
+    def call(scales=PTR, n=2, rows=64, cols=256, tiled=PTR):
+        return M.lib().moe_mxfp4_tile_scales(scales, n, rows, cols, tiled, None)
+
+    for kw in (dict(n=-1), dict(rows=0), dict(cols=0), dict(scales=None), dict(tiled=None), dict(scales=PTR + 4),
+               dict(tiled=PTR + 8)):
+        assert call(**kw) == M.MOE_ERR_INVALID_ARG, kw
+    for kw in (dict(cols=192), dict(n=1 << 40)):
+        assert call(**kw) == M.MOE_ERR_UNSUPPORTED, kw
+    assert call(n=0) == M.MOE_OK
+    assert M.moe_kernel_launches() == n0
+    with pytest.raises(ValueError):
+        M.moe_mxfp4_tile_scales(torch.zeros(4, 8, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        M.moe_mxfp4_tile_scales(torch.zeros(1, 4, 8))
+
+
+def test_matmul_binding_checks_sizes():
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    s = M.make_mxfp4_shape(4, 64, 128, 2, 1, M.MOE_ACT_NONE, M.MOE_F32)
+    good = dict(a=u8(256), a_scales=u8(16), seg_offsets=torch.zeros(2, dtype=torch.int32),
+                seg_mat=torch.zeros(1, dtype=torch.int32), w=u8(2 * 64 * 64), w_scales=u8(2 * 64 * 4),
+                bias=torch.zeros(128), y=torch.zeros(256), y_scales=None, ws=u8(256))
+    for k in ("a", "a_scales", "seg_offsets", "seg_mat", "w", "w_scales", "bias", "y"):
+        bad = dict(good)
+        bad[k] = good[k][:-1]
+        with pytest.raises(ValueError, match=k + " is smaller"):
+            M.moe_mxfp4_matmul(s, *bad.values())
