@@ -319,7 +319,8 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
  * In every mode x and out are bf16, biases and W_r fp32; FP8 scales are powers
  * of two.
  * Errors: MOE_ERR_UNSUPPORTED for MOE_F32, for T > MOE_FEW_MAX_TOKENS, and for
- * d_model or a d_ff that is not a multiple of 64 (bf16) or 128.
+ * d_model or a d_ff that is not a multiple of 64 (bf16) or 128, for d_model
+ * above 131072, and for experts reached whose weights number above 2^40.
  * ws: moe_few_workspace_size() bytes, 256-byte aligned, zero-filled once by
  * moe_few_workspace_init before first use and left consistent by every call;
  * calls that overlap on the GPU need one each.  moe_get_device_status reads

@@ -840,8 +840,8 @@ __device__ __forceinline__ void router_and_x(const Ctx& c) {
     // tokens' slices in the ring's memory
     const int sharers = gridDim.x / p.ks, who = blockIdx.x / p.ks, ks = blockIdx.x % p.ks;
     __nv_bfloat16* xsm = reinterpret_cast<__nv_bfloat16*>(c.smem + OFF_RING);
-    if (who < sharers) {
-        const int e0 = p.E * who / sharers, e1 = p.E * (who + 1) / sharers;
+    const int e0 = p.E * who / sharers, e1 = p.E * (who + 1) / sharers;
+    if (who < sharers && e0 < e1) {
         const int k0 = ks * p.slice, len = min(p.slice, p.d - k0);       // multiples of 64
         // a token's slice and zeros up to the width that a warp computes
         constexpr int W8 = SLICE_PIECES * 16;

@@ -169,6 +169,13 @@ int validate_few(const moe_config* cfg, Dims* dm) {
     // the rows of all experts are counted in 32 bits, 16 at a time
     const long long rows = static_cast<long long>(dm->E) * dm->dff + static_cast<long long>(dm->S) * dm->dffs;
     if (rows > (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+    // A block has one slice of the router (1792 columns), the selection stages
+    // the slices' partial logits of at least one token in 207 KB, and the work
+    // is counted in slots of 2 x 128 x 64 to 256 weights, in 32 bits.
+    if (dm->d > 131072) return MOE_ERR_UNSUPPORTED;
+    auto up = [](long long n) { return (n + 127) / 128; };
+    const long long act = dm->T * dm->K < dm->E ? dm->T * dm->K : dm->E;
+    if ((act * up(dm->dff) + dm->S * up(dm->dffs)) * up(dm->d) > (1ll << 26)) return MOE_ERR_UNSUPPORTED;
     dm->dtype = cfg->dtype;
     return MOE_OK;
 }

@@ -66,3 +66,16 @@ def test_pointers():
     assert M.lib().moe_few_workspace_init(ctypes.byref(config()), None, None) == M.MOE_ERR_INVALID_ARG
     assert M.lib().moe_layer_forward_few(None, *([PTR] * 23), None) == M.MOE_ERR_INVALID_ARG
     assert M.moe_kernel_launches() == n0
+
+
+@pytest.mark.parametrize("dtype", [M.MOE_BF16, M.MOE_FP8_E4M3_BLOCK, M.MOE_MXFP4])
+def test_widths_beyond_the_kernels_counting(dtype):
+    """d_model up to which every slice of the router has a block; weights counted in 32 bits."""
+    assert size(config(dtype=dtype, d_model=131072))[0] == M.MOE_OK
+    wide = config(dtype=dtype, d_model=131072 + 128)
+    long = config(dtype=dtype, T=16, d_model=131072, d_ff=131072, n_routed=256, top_k=8)
+    n0 = M.moe_kernel_launches()
+    for cfg in (wide, long):
+        assert size(cfg)[0] == M.MOE_ERR_UNSUPPORTED
+        assert call(cfg) == M.MOE_ERR_UNSUPPORTED
+    assert M.moe_kernel_launches() == n0

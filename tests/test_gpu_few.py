@@ -300,3 +300,75 @@ def test_fp8_scales_that_differ_from_block_to_block():
 def test_rows_past_one_job_and_wide_layers():
     """d_model above 128 output rows per block on the whole device (two row ranges), MXFP4."""
     check(shape(2, 128 * 152, 2, 1, 128), FP4, seed=1)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_more_columns_than_one_job_holds(kind):
+    """A row of weights longer than 64 pieces (of 64, 128 or 256 columns), with an odd number of them."""
+    long = 128 * 129 if kind != FP4 else 128 * 259
+    check(shape(3, long, 4, 2, 128, 1, 128), kind, seed=2)
+    check(shape(3, 128, 4, 2, long, 1, 128), kind, seed=3)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_work_in_large_and_small_shares(kind):
+    """Enough weights that a block has 64 slots and more in both phases, where the last shares are small."""
+    T, E, dff = 2, 4, 8448
+    d = {BF16: 4608, FP8: 9216, FP4: 18432}[kind]
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def weights(rows, cols):
+        """(stack as the layer takes it, its scales, expert e's matrix in fp64)."""
+        if kind == FP4:
+            codes = torch.randint(0, 256, (E, rows, cols // 2), dtype=torch.uint8, device="cuda", generator=gen)
+            scales = torch.randint(118, 121, (E, rows, cols // 32), dtype=torch.uint8, device="cuda", generator=gen)
+
+            def plain(e):
+                out = torch.empty((rows, cols), device="cuda")
+                M.moe_mxfp4_dequantize(codes[e], scales[e], out)
+                return out.double()
+            return codes, scales, plain
+        w = torch.randn((E, rows, cols), device="cuda", generator=gen)
+        if kind == BF16:
+            w = (w / cols ** 0.5).bfloat16()
+            return w, None, lambda e: w[e].double()
+        w = w.to(torch.float8_e4m3fn)
+        scales = 2.0 ** torch.randint(-8, -5, (E, (rows + 127) // 128, cols // 128), device="cuda", generator=gen)
+        grid = lambda e: scales[e].double().repeat_interleave(128, 0).repeat_interleave(128, 1)[:rows]  # noqa: E731
+        return w.view(torch.uint8), scales, lambda e: w[e].double() * grid(e)
+
+    W1, s1, plain1 = weights(dff, d)
+    W2, s2, plain2 = weights(d, dff)
+    f32 = lambda *n: torch.randn(n, device="cuda", generator=gen) / 8  # noqa: E731
+    inp = dict(x=torch.randn((T, d), device="cuda", generator=gen).bfloat16(), W_r=f32(E, d) / d ** 0.5, logit_bias=None,
+               W1=W1, W1_scales=s1, b1=f32(E, dff), W2=W2, W2_scales=s2, b2=f32(E, d), Ws1=None, Ws1_scales=None,
+               bs1=None, Ws2=None, Ws2_scales=None, bs2=None)
+    o = run(shape(T, d, E, E, dff), kind, inp)
+    x = inp["x"].double()
+    q = lambda v: torch.tensor(O.dequant_rows_1x128(*O.quantize_rows_1x128(v.cpu().numpy()))).cuda()  # noqa: E731
+    if kind == FP8:
+        x = q(x)
+    want = torch.zeros((T, d), dtype=torch.float64, device="cuda")
+    for e in range(E):
+        h = torch.nn.functional.silu(x @ plain1(e).T + inp["b1"][e].double())
+        y = (q(h) if kind == FP8 else h) @ plain2(e).T + inp["b2"][e].double()
+        want += torch.where(o.topk_idx == e, o.gates, 0.0).sum(1, dtype=torch.float64)[:, None] * y
+    # as in check(): the output's rounding, and an FP8 h that rounds to the other side of a border
+    assert float((o.out.double() - want).norm() / want.norm()) < (1e-2 if kind == FP8 else 5e-3)
+    first = o.out.clone()
+    for _ in range(5):
+        o.forward_few(inp["x"])
+        assert torch.equal(o.out, first)
+
+
+def test_fp8_scales_far_apart_within_a_row():
+    """Scales of neighbouring column blocks that differ by up to 2^16."""
+    sh = shape(4, 1152, 3, 2, 640, 1, 256)
+    inp, plain = inputs(sh, FP8, 13)
+    gen = torch.Generator().manual_seed(2)
+    for n in WEIGHTS:
+        s = inp[n + "_scales"]
+        m = torch.randint(-8, 9, s.shape, generator=gen).cuda()
+        s.mul_(2.0 ** m)
+        plain[n] = plain[n] * np.repeat(np.repeat(2.0 ** m.double().cpu().numpy(), 128, 1), 128, 2)
+    check(sh, FP8, inp=inp, plain=plain)
