@@ -12,7 +12,7 @@
 // columns 448..495: two slots of 24, used in turn by the K stages.  The
 // epilogue drains the 64 overlapping columns first.
 //
-// Per CTA (320 threads):
+// Per CTA (480 threads):
 //   warp 0      TMA producer: 128 bytes of K (256 elements) per stage, A 16 KB
 //               and B 32 KB;
 //   warp 1      MMA issuer: per stage copies the scales from shared to tensor
@@ -20,17 +20,19 @@
 //               then 4 MMAs of K = 64.  The warp runs the loop as a whole and
 //               one elected lane issues, so that descriptors are warp-uniform
 //               (a loop that one lane runs alone took 2600 cycles a stage);
-//   warps 2..5  epilogue: bias, SiLU, and bf16, fp32 or MXFP4 rows (a chunk
-//               of 32 columns per tcgen05.ld is one block of the output),
-//               which leave through shared memory, 64 bytes of a row at a time,
-//               so that a store instruction writes whole sectors of 8 rows (a
-//               row a lane, 16 bytes at a time, cost a third of the kernel);
-//   warps 6..9  scale loaders: a thread reads the 8 scale bytes of its A row
+//   warps 2..9  epilogue, two warps per quadrant of tensor memory (with one the
+//               epilogue was busy 95 % of the time): bias, SiLU, and bf16, fp32
+//               or MXFP4 rows (a chunk of 32 columns is one block of the
+//               output), stored a 32-byte sector of its row per lane;
+//   warps 10..13 scale loaders: a thread reads the 8 scale bytes of its A row
 //               and of two weight rows for a stage (LOOKAHEAD stages early)
 //               and lays them out in shared memory as tcgen05.cp reads them:
 //               512 bytes per 128 rows and 128 elements of K, row r's four
-//               bytes at 16 (r mod 32) + 4 (r div 32).  The MMA warp, which has
-//               nothing else in flight, makes the proxy fence.
+//               bytes at 16 (r mod 32) + 4 (r div 32).  Their scattered reads
+//               are later than the TMA's: with a ring twice as long as the
+//               codes' they run ahead of them (4096-token experts 1041 -> 952 us);
+//   warp 14     relay: makes the proxy fence for a slot of scales, which in a
+//               loader would wait for the reads it has in flight.
 // Every wait is bounded (common.cuh).
 #include "ffn_common.cuh"
 #include "mxfp4.cuh"
@@ -40,27 +42,25 @@ namespace {
 
 using namespace ffn;
 
-constexpr int NUM_THREADS = 320;
+constexpr int EPI_WARPS = 8, LOADERS = 2 + EPI_WARPS, RELAY = LOADERS + 4, NUM_THREADS = 32 * (RELAY + 1);
 constexpr int BN = 256, BKB = 128;                   // weight rows per tile; bytes of K per stage (256 elements)
-constexpr int STAGES = 4;
 constexpr uint32_t TMEM_COLS = 512, ACC1_COL = 192, SF_COL0 = 448, SF_STRIDE = 24;
-constexpr uint32_t FULL_ARRIVALS = 1 + 4;            // TMA expect_tx + one lane per loader warp
 constexpr int LOOKAHEAD = 4;                         // stages of scales a loader has in flight in registers
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 constexpr uint64_t kDrainTimeoutNs = 200000000ull;
 
+constexpr int STAGES = 4, SF_STAGES = 2 * STAGES;     // scales run ahead of the codes
 constexpr int A_BYTES = BM * BKB, B_BYTES = BN * BKB;
 constexpr int SF_BYTES = 2 * 3 * 512;                // per half stage: A, B rows 0..127, B rows 128..255
 constexpr int OFF_A = 0;
 constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
 constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
-constexpr int OFF_BAR = OFF_SF + STAGES * SF_BYTES;
-constexpr int N_BARS = 2 * STAGES + 4 + 2;           // full, empty [STAGES]; accf, acce [2]; ovl; drain
+constexpr int OFF_BAR = OFF_SF + SF_STAGES * SF_BYTES;
+constexpr int N_BARS = STAGES + 3 * SF_STAGES + 4 + 2;   // full; empty, sfull, sready; accf, acce [2]; ovl; drain
 constexpr int OFF_MISC = OFF_BAR + N_BARS * 8;
 constexpr int OFF_SEG = OFF_MISC + 16;
 constexpr int OFF_BIAS = (OFF_SEG + SegTable::SEG_INTS * 4 + 15) & ~15;   // 2 x BN fp32, the tiles in flight
-constexpr int OFF_OUT = (OFF_BIAS + 2 * BN * 4 + 127) & ~127;             // per epilogue warp, 32 rows x 64 bytes of output
-constexpr int TOTAL = OFF_OUT + 4 * 32 * 64;
+constexpr int TOTAL = OFF_BIAS + 2 * BN * 4;
 constexpr int ALLOC = TOTAL + 1024;
 static_assert(ALLOC <= 227 * 1024, "shared memory budget");
 static_assert(OFF_SF % 128 == 0 && OFF_BAR % 8 == 0, "alignment");
@@ -71,6 +71,7 @@ struct __align__(64) Mx4Params {
     const uint8_t* a_scales;  // (rows, K/32)
     const uint8_t* w_scales;  // (n_mats, N, K/32)
     uint8_t* y_scales;        // (rows, N/32), MXFP4 output
+    int wide_rows;            // y's rows start on 32-byte boundaries
 };
 
 // The MMA thread's wait for a full stage: bounded, polling without the
@@ -106,7 +107,9 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* empty = full + STAGES;
-    uint64_t* accf = empty + STAGES;
+    uint64_t* sfull = empty + SF_STAGES;
+    uint64_t* sready = sfull + SF_STAGES;
+    uint64_t* accf = sready + SF_STAGES;
     uint64_t* acce = accf + 2;
     uint64_t* ovl = acce + 2;
     uint64_t* drain = ovl + 1;
@@ -117,9 +120,10 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
 
     if (warp == 0) tmem_alloc<TMEM_COLS>(tmem_slot);
     if (warp == 1 && lane == 0) {
-        for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], FULL_ARRIVALS); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], 128); }
-        mbar_init(ovl, 128);
+        for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < SF_STAGES; ++i) { mbar_init(&empty[i], 1); mbar_init(&sfull[i], 4); mbar_init(&sready[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&accf[i], 1); mbar_init(&acce[i], EPI_WARPS); }
+        mbar_init(ovl, EPI_WARPS);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -136,16 +140,20 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
     const int K = p.g[0].K, N = p.g[0].N;
     const int kblocks = ceil_div(K, 2 * BKB);
 
+    // Item i (a K stage of a tile, counted over the CTA's tiles) has its codes
+    // in stage i mod STAGES and its scales in slot i mod SF_STAGES; empty[slot]
+    // reports its MMAs done.
     if (warp == 0) {
         // ================= TMA producer
         if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
+            int stage = 0, issued = 0, slot = SF_STAGES - STAGES;        // slot: of the item STAGES before
+            uint32_t phase = 0, eph = 1;
             bool ok = true;
             for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
                 const TileInfo ti = decode_tile<BN, 2 * BKB>(tile, p, seg, nseg);
                 for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                    if (!mbar_wait_bounded(&empty[slot], eph, abort_flag, p.status, p.timeout_ns)) { ok = false; break; }
+                    if (++slot == SF_STAGES) { slot = 0; eph ^= 1u; }
                     mbar_arrive_expect_tx(&full[stage], A_BYTES + B_BYTES);
                     tma_load_2d(smem + OFF_A + stage * A_BYTES, &p.a_map[0], &full[stage], kb * BKB, ti.a_row);
                     tma_load_3d(smem + OFF_B + stage * B_BYTES, &p.b_map[0], &full[stage], kb * BKB, ti.n0, ti.mat);
@@ -173,8 +181,8 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
             if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
             return __all_sync(0xffffffffu, mma_wait_spin(bar, parity, abort_flag, p.status, p.timeout_ns)) != 0;
         };
-        int stage = 0, abuf = 0, item = 0;
-        uint32_t phase = 0, aph0 = 0, aph1 = 0, ovl_ph = 0;
+        int stage = 0, sslot = 0, abuf = 0, item = 0;
+        uint32_t phase = 0, sph = 0, aph0 = 0, aph1 = 0, ovl_ph = 0;
         bool ok = true, first = true;
 #pragma unroll 1
         for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
@@ -191,18 +199,17 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
             const uint32_t d_tmem = tmem_base + (abuf ? ACC1_COL : 0u);
 #pragma unroll 1
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!wait(&full[stage], phase)) { ok = false; break; }
-                fence_proxy_async_smem();
-                // the MMAs that read this scale slot two stages ago are done
+                if (!wait(&sready[sslot], sph) || !wait(&full[stage], phase)) { ok = false; break; }
+                // the MMAs that read this slot of tensor memory two items ago are done
                 if (item >= 2) {
-                    const int s2 = (stage + STAGES - 2) % STAGES;
-                    if (!wait(&empty[s2], stage >= 2 ? phase : phase ^ 1u)) { ok = false; break; }
+                    const int s2 = (sslot + SF_STAGES - 2) % SF_STAGES;
+                    if (!wait(&empty[s2], sslot >= 2 ? sph : sph ^ 1u)) { ok = false; break; }
                 }
                 item = item < 2 ? item + 1 : 2;
                 tc_fence_after();
                 const uint64_t adesc = smem_desc_k_sw128(smem + OFF_A + stage * A_BYTES);
                 const uint64_t bdesc = smem_desc_k_sw128(smem + OFF_B + stage * B_BYTES);
-                const uint8_t* sf = smem + OFF_SF + stage * SF_BYTES;
+                const uint8_t* sf = smem + OFF_SF + sslot * SF_BYTES;
                 const uint32_t slot = tmem_base + SF_COL0 + static_cast<uint32_t>(stage & 1) * SF_STRIDE;
                 if (leader) {
 #pragma unroll
@@ -213,9 +220,10 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
                         umma_mxf4_bs(d_tmem, adesc + 2 * k, bdesc + 2 * k, make_idesc_mxf4(BN, 2 * (k & 1)), s, s + 4,
                                      (kb > 0 || k > 0) ? 1u : 0u);
                     }
-                    umma_commit(&empty[stage]);
+                    umma_commit(&empty[sslot]);
                 }
                 __syncwarp();
+                if (++sslot == SF_STAGES) { sslot = 0; sph ^= 1u; }
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
             if (!ok) break;
@@ -230,28 +238,33 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
             mbar_wait_bounded(drain, 0, &no_abort, nullptr, kDrainTimeoutNs);
         }
         __syncwarp();
-    } else if (warp < 6) {
-        // ================= epilogue (warps 2..5)
-        const int quad = warp & 3;
+    } else if (warp < LOADERS) {
+        // ================= epilogue (warps 2..9)
+        const int quad = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        auto arrive = [&](uint64_t* bar) {                 // the warp's reads of tensor memory are done
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         int abuf = 0;
         uint32_t fph0 = 0, fph1 = 0;
         bool ok = true;
         for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x) {
             const TileInfo ti = decode_tile<BN, 2 * BKB>(tile, p, seg, nseg);
             const GroupDev& g = p.g[0];
-            // the tile's biases, a quarter from each warp; the buffer's tile from
+            // the tile's biases, an eighth from each warp; the buffer's tile from
             // two tiles back is done with in every warp, which all were here
             // for the tile between
             float* bias_s = reinterpret_cast<float*>(smem + OFF_BIAS) + abuf * BN;
-            if (lane < 16) {
-                const int i = quad * 64 + 4 * lane;
+            if (lane < 8) {
+                const int i = (warp - 2) * 32 + 4 * lane;
                 const float4 v = (g.bias && ti.n0 + i < N)
                     ? __ldg(reinterpret_cast<const float4*>(g.bias + static_cast<size_t>(ti.mat) * N + ti.n0 + i))
                     : make_float4(0.f, 0.f, 0.f, 0.f);
                 *reinterpret_cast<float4*>(bias_s + i) = v;
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, 256;" ::: "memory");
             uint32_t& fph = abuf ? fph1 : fph0;
             // (after a wait gave up the warps keep meeting at the barrier above)
             if (ok) ok = warp_wait(&accf[abuf], fph, abort_flag, p.status, p.timeout_ns, lane);
@@ -261,100 +274,110 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
             const uint32_t acc = lane_base + (abuf ? ACC1_COL : 0u);
             const size_t row0 = static_cast<size_t>(ti.c_row + quad * 32);       // the warp's first row
             const int rows = min(32, ti.rows_left - quad * 32);                  // of them valid (may be negative)
-            uint8_t* stage = smem + OFF_OUT + quad * 32 * 64;
-            // 16-byte chunk q of row r of the staging is at q ^ ((r >> 1) & 3),
-            // which spreads the lanes' writes and reads over the banks
-            auto put = [&](int q, const uint4& v) {
-                *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = v;
-            };
-            // the warp's rows, 64 bytes each, to byte `at` of rows of `pitch` bytes; only `bytes` of them
-            auto flush = [&](size_t pitch, size_t at, int bytes) {
-                __syncwarp();
-#pragma unroll
-                for (int r8 = 0; r8 < 32; r8 += 8) {
-                    const int r = r8 + (lane >> 2), q = lane & 3;
-                    if (r < rows && 16 * q < bytes)
-                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + (row0 + r) * pitch + at + 16 * q) =
-                            *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+            // 32 bytes (a sector) of the lane's row, at byte `at` of rows of `pitch` bytes
+            auto put = [&](size_t pitch, size_t at, const uint32_t* w) {
+                if (lane >= rows) return;
+                uint8_t* dst = static_cast<uint8_t*>(g.C) + (row0 + lane) * pitch + at;
+                if (mp.wide_rows) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" :: "l"(dst), "r"(w[0]), "r"(w[1]),
+                                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+                } else {
+                    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
-                __syncwarp();
             };
-            // chunks of 32 columns, the overlapping ones (6, 7 of buffer 0;
-            // 0, 1 of buffer 1) first
+            // Pairs of 32-column chunks; a warp half has two of the four, the
+            // first half the overlapping one (the last pair of buffer 0, the
+            // first of buffer 1) first.
 #pragma unroll 1
-            for (int ci = 0; ci < BN / 32; ++ci) {
-                const int c = abuf ? ci : (ci + 6) & 7;
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c * 32), r);
-                tmem_ld_wait_regs(r);
-                if (ci == 1) { tc_fence_before(); mbar_arrive(ovl); }
-                else if (ci == BN / 32 - 1) { tc_fence_before(); mbar_arrive(&acce[abuf]); }
-                const int n = ti.n0 + c * 32;
-                if (rows <= 0 || n >= N) continue;               // (the same for the whole warp)
-                float v[32];
-                const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
+            for (int i = 0; i < 2; ++i) {
+                const int c0 = 2 * ((2 * i + half + (abuf ? 0 : 3)) & 3);
+                uint32_t r[2][32];
+                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c0 * 32), r[0]);
+                tmem_ld_32x32b_x32(acc + static_cast<uint32_t>(c0 * 32 + 32), r[1]);
+                tmem_ld_wait_regs(r[0]);
+                tmem_ld_wait_regs(r[1]);
+                arrive(i == 0 ? ovl : &acce[abuf]);
+                uint32_t w4[8];                                  // MXFP4: the pair's 64 columns are 32 bytes of a row
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 b = b4[j];
-                    v[4 * j + 0] = __uint_as_float(r[4 * j + 0]) + b.x;
-                    v[4 * j + 1] = __uint_as_float(r[4 * j + 1]) + b.y;
-                    v[4 * j + 2] = __uint_as_float(r[4 * j + 2]) + b.z;
-                    v[4 * j + 3] = __uint_as_float(r[4 * j + 3]) + b.w;
-                }
-                if (p.silu) {
+                for (int u = 0; u < 2; ++u) {
+                    const int c = c0 + u, n = ti.n0 + c * 32;
+                    if (rows <= 0 || n >= N) continue;           // (the same for the whole warp)
+                    float v[32];
+                    const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
-                }
-                if constexpr (OUT == MOE_F32) {
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 b = b4[j];
+                        v[4 * j + 0] = __uint_as_float(r[u][4 * j + 0]) + b.x;
+                        v[4 * j + 1] = __uint_as_float(r[u][4 * j + 1]) + b.y;
+                        v[4 * j + 2] = __uint_as_float(r[u][4 * j + 2]) + b.z;
+                        v[4 * j + 3] = __uint_as_float(r[u][4 * j + 3]) + b.w;
+                    }
+                    if (p.silu) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                        for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
+                    }
+                    if constexpr (OUT == MOE_F32) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float* f = v + 16 * h + 4 * q;
-                            put(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                              __float_as_uint(f[3])));
+                            uint32_t w[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * q + j]);
+                            put(4 * static_cast<size_t>(N), 4 * static_cast<size_t>(n + 8 * q), w);
                         }
-                        flush(4 * static_cast<size_t>(N), 4 * static_cast<size_t>(n + 16 * h), 64);
-                    }
-                } else if constexpr (OUT == MOE_BF16) {
+                    } else if constexpr (OUT == MOE_BF16) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[4];
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w[8];
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * q + 2 * h], v[8 * q + 2 * h + 1]);
-                            w[h] = *reinterpret_cast<uint32_t*>(&t);
+                            for (int j = 0; j < 8; ++j) {
+                                __nv_bfloat162 t = __floats2bfloat162_rn(v[16 * q + 2 * j], v[16 * q + 2 * j + 1]);
+                                w[j] = *reinterpret_cast<uint32_t*>(&t);
+                            }
+                            put(2 * static_cast<size_t>(N), 2 * static_cast<size_t>(n + 16 * q), w);
                         }
-                        put(q, make_uint4(w[0], w[1], w[2], w[3]));
+                    } else {
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+                        const uint32_t sb = mxfp4_scale_byte(m);
+                        const float inv = mxfp4_inv_scale(sb == 255u ? 127u : sb);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            float t[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) t[j] = v[8 * q + j] * inv;
+                            w4[4 * u + q] = sb == 255u ? 0u : f32x8_to_e2m1x8(t);
+                        }
+                        if (lane < rows) mp.y_scales[((row0 + lane) * N + n) / 32] = static_cast<uint8_t>(sb);
+                        const size_t pitch = static_cast<size_t>(N) / 2, at = static_cast<size_t>(ti.n0 + c0 * 32) / 2;
+                        if (u == 1) put(pitch, at, w4);
+                        else if (n + 32 >= N && lane < rows)     // the row's last 32 columns alone
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + (row0 + lane) * pitch + at) =
+                                make_uint4(w4[0], w4[1], w4[2], w4[3]);
                     }
-                    flush(2 * static_cast<size_t>(N), 2 * static_cast<size_t>(n), 64);
-                } else {
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-                    const uint32_t sb = mxfp4_scale_byte(m);
-                    const float inv = mxfp4_inv_scale(sb == 255u ? 127u : sb);
-                    uint32_t w[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float t[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) t[j] = v[8 * q + j] * inv;
-                        w[q] = sb == 255u ? 0u : f32x8_to_e2m1x8(t);
-                    }
-                    // chunks come in runs of 4 (6 7 0 1 | 2 3 4 5, or 0 1 2 3 | 4 5 6 7) of
-                    // which two neighbours make 32 bytes of a row: one sector
-                    put(c & 1, make_uint4(w[0], w[1], w[2], w[3]));
-                    if (lane < rows) mp.y_scales[((row0 + lane) * N + n) / 32] = static_cast<uint8_t>(sb);
-                    if ((c & 1) || n + 32 >= N)
-                        flush(static_cast<size_t>(N) / 2, (static_cast<size_t>(n) - (c & 1) * 32) / 2, 16 * ((c & 1) + 1));
                 }
             }
             abuf ^= 1;
         }
+    } else if (warp == RELAY) {
+        // ================= scales: every loader's part of a slot is there, made visible to the copies to tensor memory
+        int slot = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int tile = blockIdx.x; tile < total_tiles && ok; tile += gridDim.x) {
+#pragma unroll 1
+            for (int kb = 0; kb < kblocks; ++kb) {
+                if (!warp_wait(&sfull[slot], ph, abort_flag, p.status, p.timeout_ns, lane)) { ok = false; break; }
+                fence_proxy_async_smem();
+                if (lane == 0) mbar_arrive(&sready[slot]);
+                if (++slot == SF_STAGES) { slot = 0; ph ^= 1u; }
+            }
+        }
     } else {
-        // ================= scale loaders (warps 6..9): thread i has A row i and weight rows i, 128 + i
-        const int i = tid - 6 * 32;
+        // ================= scale loaders (warps 10..13): thread i has A row i and weight rows i, 128 + i
+        const int i = tid - LOADERS * 32;
         const int kq = K / 32;                           // scale bytes per row, a multiple of 4
         uint32_t* dst0 = reinterpret_cast<uint32_t*>(smem + OFF_SF + 16 * (i & 31) + 4 * (i >> 5));
         auto start = [&](Item& it) {
@@ -391,17 +414,17 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
         Item cur, ahead;
         start(cur);
         start(ahead);
-        int stage = 0;
+        int slot = 0;
         uint32_t phase = 0;
         bool aborted = false;
         auto store = [&](const uint32_t (&v)[6]) {
-            if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.timeout_ns, lane)) { aborted = true; return; }
-            uint32_t* dst = dst0 + stage * (SF_BYTES / 4);
+            if (!warp_wait(&empty[slot], phase ^ 1u, abort_flag, p.status, p.timeout_ns, lane)) { aborted = true; return; }
+            uint32_t* dst = dst0 + slot * (SF_BYTES / 4);
 #pragma unroll
             for (int q = 0; q < 6; ++q) dst[q * 128] = v[q];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[stage]);
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            if (lane == 0) mbar_arrive(&sfull[slot]);
+            if (++slot == SF_STAGES) { slot = 0; phase ^= 1u; }
             advance(cur);
         };
         if (kq % 16 == 0) {
@@ -493,6 +516,8 @@ cudaError_t launch_mxfp4_matmul(const moe_mxfp4_shape& s, const uint8_t* a, cons
     p.a_scales = a_scales;
     p.w_scales = w_scales;
     p.y_scales = y_scales;
+    const size_t pitch = static_cast<size_t>(s.n) * (s.out_dtype == MOE_F32 ? 32 : s.out_dtype == MOE_BF16 ? 16 : 4) / 8;
+    p.wide_rows = (reinterpret_cast<uintptr_t>(y) | pitch) % 32 == 0;
     if (!encode_tma_2d(&p.tc.a_map[0], a, s.rows, s.k / 2, 1, BM) ||
         !encode_tma_3d(&p.tc.b_map[0], w, s.n_mats, s.n, s.k / 2, 1, BN))
         return cudaErrorInvalidValue;
