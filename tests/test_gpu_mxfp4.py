@@ -311,3 +311,36 @@ def test_experts_of_a_layer_in_four_bits(seed, T, d, E, K, dff):
     got = few.forward_few(g["x"][:n])[0].double().cpu().numpy()
     assert np.array_equal(few.topk_idx.cpu().numpy(), idx_h[:n])
     assert rel(got, exact[:n]) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("k", [512, 1536, 2560, 4608])
+def test_matmul_rows_of_scales_that_end_inside_a_read(k):
+    y, _, z, S, end = product([130, 3, 90], [1, 0, 1], 2, 320, k, M.MOE_ACT_NONE, M.MOE_F32, behind=1, seed=k)
+    want, tol = bounds(z, S, k, M.MOE_ACT_NONE)
+    assert np.all(np.abs(y.double().numpy() - want)[:end] <= tol[:end] + 1e-37)
+
+
+@pytest.mark.parametrize("out", [M.MOE_F32, M.MOE_BF16, M.MOE_MXFP4])
+def test_matmul_operands_on_16_byte_boundaries(out):
+    """The same bits whatever the multiple of 16 bytes at which scales and output start."""
+    k, n, rows = 2048, 192, 200
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    (ac, asc), (wc, wsc) = (quantize(torch.randn(r, k, device="cuda", generator=gen)) for r in (rows, n))
+    offs, mats = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, rows], [0]))
+    s = M.make_mxfp4_shape(rows, n, k, 1, 1, M.MOE_ACT_SILU, out)
+    ws = torch.zeros(M.moe_mxfp4_workspace_size(s), dtype=torch.uint8, device="cuda")
+    size = rows * n * {M.MOE_F32: 8, M.MOE_BF16: 4, M.MOE_MXFP4: 1}[out] // 2
+
+    def at(off, t):
+        buf = torch.zeros(t.numel() + 64, dtype=torch.uint8, device="cuda")
+        buf[off:off + t.numel()] = t.reshape(-1)
+        return buf[off:off + t.numel()]
+
+    got = []
+    for off in (0, 16):
+        y = at(off, torch.zeros(size, dtype=torch.uint8, device="cuda"))
+        ysc = torch.zeros((rows, n // 32), dtype=torch.uint8, device="cuda") if out == M.MOE_MXFP4 else None
+        M.moe_mxfp4_matmul(s, ac, at(off, asc), offs, mats, wc, at(off, wsc), None, y, ysc, ws)
+        got.append((y.clone(), ysc))
+    assert torch.equal(got[0][0], got[1][0]) and bool(got[0][0].any())
+    assert out != M.MOE_MXFP4 or torch.equal(got[0][1], got[1][1])
