@@ -8,8 +8,11 @@ fallback: if the shared library is missing, importing the entry points raises.
 Entry points (same names as the C ABI): moe_workspace_size, moe_buffer_rows,
 moe_workspace_init, moe_get_device_status, moe_route, moe_dispatch,
 moe_expert_ffn, moe_combine, moe_balance_stats, moe_layer_forward,
-moe_selftest_wait_timeout.  `MoELayer` bundles a config, its workspace and
-its weights for the common whole-layer call.
+moe_selftest_wait_timeout; for serving moe_layer_forward_few (at most 16
+tokens in one kernel), moe_mxfp4_quantize, moe_mxfp4_dequantize,
+moe_mxfp4_tile_scales and moe_mxfp4_matmul (shapes from make_mxfp4_shape).
+`MoELayer` bundles a config, its workspace and its weights for the common
+whole-layer calls.
 """
 from __future__ import annotations
 
@@ -440,16 +443,15 @@ class MoELayer:
         self.w = weights
         self.device = torch.device(device)
         if cfg.dtype == MOE_MXFP4:
-            self.ws = self._few_workspace()
             self.w = dict(weights)
             for k in ("W1_scales", "W2_scales", "Ws1_scales", "Ws2_scales"):
                 if weights.get(k) is not None:
                     self.w[k] = moe_mxfp4_tile_scales(weights[k])
+            self.ws = self._few_workspace()
         else:
             self.ws = torch.empty(moe_workspace_size(cfg), dtype=torch.uint8, device=self.device)
             moe_workspace_init(cfg, self.ws)
         self._few_ws = self.ws if cfg.dtype == MOE_MXFP4 else None
-        self._few_known = None                                 # the tensors whose layout forward_few has checked
         self._cfg_ref = ctypes.byref(cfg)
         out_dt = torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16
         self.out = torch.empty((cfg.T, cfg.d_model), dtype=out_dt, device=self.device)
@@ -470,7 +472,22 @@ class MoELayer:
         return self.out, self.f, self.P, self.loss
 
     def _few_workspace(self):
+        """The few-token layer's workspace; refuses weights smaller than the layer's shape says."""
         import torch
+        c = self.cfg
+        bits = {MOE_BF16: 16, MOE_FP8_E4M3_BLOCK: 8, MOE_MXFP4: 4}.get(c.dtype, 0)
+        scale = {MOE_FP8_E4M3_BLOCK: 4, MOE_MXFP4: 512}.get(c.dtype, 0)      # bytes per 128 x 128 block
+        up = lambda n: (n + 127) // 128  # noqa: E731
+        need = {"W_r": 4 * c.n_routed * c.d_model, "logit_bias": 4 * c.n_routed}
+        for p, e, ff in (("W", c.n_routed, c.d_ff), ("Ws", c.n_shared, c.d_ff_shared)):
+            for i, rows, cols in ((1, ff, c.d_model), (2, c.d_model, ff)):
+                need[f"{p}{i}"] = e * rows * cols * bits // 8
+                need[f"{p}{i}_scales"] = e * up(rows) * up(cols) * scale
+                need[f"{p.replace('W', 'b')}{i}"] = 4 * e * rows
+        for name, n in need.items():
+            t = self.w.get(name)
+            if t is not None and t.numel() * t.element_size() < n:
+                raise ValueError(f"forward_few: {name} is smaller than its shape says")
         ws = torch.empty(moe_few_workspace_size(self.cfg), dtype=torch.uint8, device=self.device)
         moe_few_workspace_init(self.cfg, ws)
         return ws
@@ -483,16 +500,10 @@ class MoELayer:
         w = self.w
         tensors = [w.get(k) for k in _FEW_WEIGHTS]
         tensors += (self.out, self.f, self.P, self.loss, self.topk_idx, self.gates, self.counts, self._few_ws)
-        known = self._few_known
-        if known is None or any(a is not b for a, b in zip(known, tensors)):
-            for t in tensors:
-                _p(t)                                          # on the GPU, dense
-            self._few_known = tensors
         if x.dtype != self.out.dtype or x.numel() != self.out.numel():
             raise ValueError("forward_few: x must be bfloat16 (T, d_model)")
         _on_current_device(x, "forward_few")
-        ptrs = [None if t is None else t.data_ptr() for t in tensors]
-        _check(lib().moe_layer_forward_few(self._cfg_ref, _p(x), *ptrs, _stream(stream)), "moe_layer_forward_few")
+        _check(lib().moe_layer_forward_few(self._cfg_ref, _p(x), *map(_p, tensors), _stream(stream)), "moe_layer_forward_few")
         return self.out, self.f, self.P, self.loss
 
     def _forward_into(self, x, out, loss, stream=None):

@@ -383,7 +383,9 @@ struct Plan {
             }
         } else {
             const int tiles = (p.d + 127) / 128, tile = p.S * ss + n_active * sr;
-            if (tiles * tile / blocks >= 64) {
+            // (with more tiles than blocks a share would have several tiles of
+            // which parts are elsewhere, and a share has room for one it begins)
+            if (tiles <= blocks && tiles * tile / blocks >= 64) {
                 tail = tile / 8;
                 q = min(tail / 10, min(SMALL * blocks / tiles, (4 * blocks + tiles - 1) / tiles));
                 if (q < 1) q = tail = 0;

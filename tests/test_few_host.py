@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import sparse_mixture_experts_20_b200 as M
 
@@ -79,3 +80,24 @@ def test_widths_beyond_the_kernels_counting(dtype):
         assert size(cfg)[0] == M.MOE_ERR_UNSUPPORTED
         assert call(cfg) == M.MOE_ERR_UNSUPPORTED
     assert M.moe_kernel_launches() == n0
+
+
+@pytest.mark.parametrize("dtype,bits", [(M.MOE_BF16, 16), (M.MOE_FP8_E4M3_BLOCK, 8), (M.MOE_MXFP4, 4)])
+def test_layer_refuses_small_weights(dtype, bits, monkeypatch):
+    """The sizes that a layer checks before its first call, on a layer without a GPU."""
+    monkeypatch.setattr(M, "moe_few_workspace_init", lambda cfg, ws: None)
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    sc = {M.MOE_FP8_E4M3_BLOCK: 4, M.MOE_MXFP4: 512}.get(dtype, 0)
+    w = dict(W_r=u8(4 * 8 * 256), logit_bias=None, b1=u8(4 * 8 * 128), b2=u8(4 * 8 * 256), bs1=u8(4 * 128),
+             bs2=u8(4 * 256), W1=u8(8 * 128 * 256 * bits // 8), W2=u8(8 * 128 * 256 * bits // 8),
+             Ws1=u8(128 * 256 * bits // 8), Ws2=u8(128 * 256 * bits // 8))
+    if sc:
+        w.update(W1_scales=u8(8 * 2 * sc), W2_scales=u8(8 * 2 * sc), Ws1_scales=u8(2 * sc), Ws2_scales=u8(2 * sc))
+    layer = M.MoELayer.__new__(M.MoELayer)
+    layer.cfg, layer.w, layer.device = config(dtype=dtype), w, torch.device("cpu")
+    layer._few_workspace()
+    for name in w:
+        if w[name] is not None:
+            layer.w = {**w, name: w[name][:-1]}
+            with pytest.raises(ValueError, match=name + " is smaller"):
+                layer._few_workspace()

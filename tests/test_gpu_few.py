@@ -310,11 +310,14 @@ def test_more_columns_than_one_job_holds(kind):
     check(shape(3, 128, 4, 2, long, 1, 128), kind, seed=3)
 
 
-@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
-def test_work_in_large_and_small_shares(kind):
-    """Enough weights that a block has 64 slots and more in both phases, where the last shares are small."""
+@pytest.mark.parametrize("kind,wide", [(BF16, 0), (FP8, 0), (FP4, 0), (BF16, 19200), (FP8, 20480)])
+def test_work_in_large_and_small_shares(kind, wide):
+    """Enough weights that a block has 64 slots and more in both phases, where the last shares are small; and more
+    tiles of output rows than there are blocks."""
     T, E, dff = 2, 4, 8448
-    d = {BF16: 4608, FP8: 9216, FP4: 18432}[kind]
+    d = wide or {BF16: 4608, FP8: 9216, FP4: 18432}[kind]
+    if wide:
+        dff = 2560 if kind == BF16 else 5120
     gen = torch.Generator(device="cuda").manual_seed(5)
 
     def weights(rows, cols):
