@@ -217,11 +217,16 @@ mxfp4_matmul_kernel(const __grid_constant__ Mx4Params mp) {
             const uint32_t d_tmem = tmem_base + (abuf ? ACC1_COL : 0u);
 #pragma unroll 1
             for (int kb = 0; kb < kblocks; ++kb) {
-                if (!wait(&sready[sslot], sph) || !wait(&full[stage], phase)) { ok = false; break; }
-                // the MMAs that read this slot of tensor memory two items ago are done
-                if (item >= 2) {
-                    const int s2 = (sslot + SF_STAGES - 2) % SF_STAGES;
-                    if (!wait(&empty[s2], sslot >= 2 ? sph : sph ^ 1u)) { ok = false; break; }
+                // its scales, its codes, and the MMAs that read this slot of
+                // tensor memory two items ago: asked for together
+                const int s2 = (sslot + SF_STAGES - 2) % SF_STAGES;
+                const uint32_t s2_ph = sslot >= 2 ? sph : sph ^ 1u;
+                const bool r0 = mbar_try_wait(&sready[sslot], sph), r1 = mbar_try_wait(&full[stage], phase),
+                           r2 = item < 2 || mbar_try_wait(&empty[s2], s2_ph);
+                if (!__all_sync(0xffffffffu, r0 && r1 && r2) &&
+                    !(wait(&sready[sslot], sph) && wait(&full[stage], phase) && (item < 2 || wait(&empty[s2], s2_ph)))) {
+                    ok = false;
+                    break;
                 }
                 item = item < 2 ? item + 1 : 2;
                 tc_fence_after();
