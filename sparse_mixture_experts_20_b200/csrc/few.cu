@@ -55,6 +55,10 @@
 // loops therefore run both phases through the same code (measured: 172 KB of
 // code took 10 us to select the experts of one token and 7 us from there to
 // the first weights).
+// Measured (7168 x 2048 experts, 256 of them, top-8 and one shared): MXFP4 one
+// token 49 us, sixteen 304 to 316 (1.62 GB, 5.1 to 5.3 TB/s); FP8 67 and 527 to
+// 538 us (3.04 GB, 5.7 TB/s); bf16, eight tokens, 8 experts of 4096 x 14336,
+// 287 us (1.69 GB, 5.9 TB/s).  The copy rate of the same GPUs is 6.5 TB/s.
 // Every wait is bounded (common.cuh); after a wait gives up, the warps skip
 // the remaining work but keep meeting at the block's barriers.
 #include <cuda.h>
