@@ -317,7 +317,8 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
  *                             not quantised: they enter as sums of five E2M1
  *                             terms, within amax / 12288 of each 32 columns
  * In every mode x and out are bf16, biases and W_r fp32; FP8 scales are powers
- * of two.
+ * of two.  out may be x itself, and overlaps nothing else.  With MXFP4 weights
+ * an infinity in x or in the hidden activation makes NaN of its token's sums.
  * Errors: MOE_ERR_UNSUPPORTED for MOE_F32, for T > MOE_FEW_MAX_TOKENS, and for
  * d_model or a d_ff that is not a multiple of 64 (bf16) or 128, for d_model
  * above 131072, and for experts reached whose weights number above 2^40.
@@ -385,7 +386,8 @@ MOE_EXPORT int moe_mxfp4_tile_scales(const uint8_t* scales, int64_t n_mats, int3
  *      zero-filled once by moe_mxfp4_workspace_init
  * Rows outside every segment are not written.  A segment whose bounds lie
  * outside [0, rows] or whose matrix is outside [0, n_mats) is skipped and sets
- * MOE_DEV_BAD_ROUTING.  Pointers 16-byte aligned. */
+ * MOE_DEV_BAD_ROUTING.  Segments do not overlap (a row of two is written by
+ * both, in no order), nor does y any operand.  Pointers 16-byte aligned. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_SILU 1
 typedef struct {

@@ -375,3 +375,38 @@ def test_fp8_scales_far_apart_within_a_row():
         s.mul_(2.0 ** m)
         plain[n] = plain[n] * np.repeat(np.repeat(2.0 ** m.double().cpu().numpy(), 128, 1), 128, 2)
     check(sh, FP8, inp=inp, plain=plain)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_two_layers_at_once_on_two_streams(kind):
+    """Each with its workspace, on streams that overlap, beside other kernels: the results of one after the other."""
+    shapes = [shape(5, 1024, 16, 4, 512, 1, 256), shape(1, 128, 8, 2, 256)]
+    made = [inputs(sh, kind, 20 + i)[0] for i, sh in enumerate(shapes)]
+    layers = [M.MoELayer(config(sh, kind), inp) for sh, inp in zip(shapes, made)]
+    want = []
+    for la, inp in zip(layers, made):
+        want.append(la.forward_few(inp["x"])[0].clone())
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [[], []]
+    busy = torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(layers[i].forward_few(made[i]["x"])[0].clone())
+        busy = busy * 1.0001
+    torch.cuda.synchronize()
+    for la, w, g in zip(layers, want, got):
+        assert all(torch.equal(w, t) for t in g)
+        assert M.moe_get_device_status(la.cfg, la._few_ws) == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_output_in_place_of_the_input(kind):
+    sh = shape(7, 512, 12, 3, 256, 1, 128, capacity_factor=0.5, overflow_mode=1)
+    inp, _ = inputs(sh, kind, 21)
+    layer = run(sh, kind, inp)
+    want = layer.out.clone()
+    layer.out.copy_(inp["x"])
+    layer.forward_few(layer.out)
+    assert torch.equal(layer.out, want)
