@@ -14,8 +14,9 @@
 //      per slice; the image of x;
 //   -- barrier; every block then selects the top-K of all tokens for itself
 //      (slices added in order) and builds the list of experts reached;
-//   2  h = SiLU(W1 x + b1); bf16: straight into its image;
-//   -- barrier; FP8 and MXFP4: the image of h, barrier;
+//   2  h = SiLU(W1 x + b1), into its image: a tile's 128 rows are 128 columns
+//      of h, which FP8 and MXFP4 scale together or in fours;
+//   -- barrier;
 //   3  out = sum over the experts of gate * (W2 h + b2), shared experts
 //      included.
 // Phases 2 and 3 are one sequence each of tiles of 128 result rows (phase 2:
@@ -45,7 +46,7 @@
 //          core has to spare.
 //
 // Per block (352 threads):
-//   warps 0..7  phase 1, selection, image of h; warps 0..3 the epilogues
+//   warps 0..7  phase 1 and selection; warps 0..3 the epilogues
 //               (thread = row);
 //   warp 8      plans the jobs of the block's shares, and loads weights and
 //               their scales;
@@ -129,7 +130,7 @@ static_assert(OFF_KPACK % 8 == 0 && OFF_BAR % 8 == 0 && OFF_JOBS % 8 == 0 && siz
 static_assert(SFA_COL0 + 32 <= TMEM_COLS && PLANES * MAX_T + 3 <= ACC_COLS, "tensor memory budget");
 
 // grid-wide counters in the workspace, zero between launches
-enum { CTR_BAR = 0, CTR_EXIT = 3, CTR_ABORT = 4, CTR_SHARE = 5, CTR_WORDS = 7, CTR_TILE = 64 };
+enum { CTR_BAR = 0, CTR_EXIT = 2, CTR_ABORT = 3, CTR_SHARE = 4, CTR_WORDS = 6, CTR_TILE = 64 };
 
 struct __align__(64) FewParams {
     CUtensorMap w1, w2, ws1, ws2;
@@ -151,7 +152,6 @@ struct __align__(64) FewParams {
     uint8_t *xq, *xs;             // image of x: rows, scales
     uint8_t *hq, *hs;             // image of h, routed
     uint8_t *hqs, *hss;           // image of h, shared
-    float* h32;                   // fp32 h: (T K, dff), then (S T, dffs)
     float* sums;                  // (shares, 2, T, 128) parts of tiles that cross shares
     float alpha;
     int T, d, E, K, dff, S, dffs, capacity, slot_major, passthrough;
@@ -324,11 +324,6 @@ __device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* st
 }
 
 // ---------------------------------------------------------------- jobs
-
-// Row of h32 for token t of a job.
-__device__ __forceinline__ int h_row(const Ctx& c, const Job& j, int t) {
-    return j.shared ? j.mat * c.p.T + t : t * c.p.K + (static_cast<int>(j.kpack >> (4 * t)) & 15);
-}
 
 // Place of token t among the columns of its expert's image of h.
 __device__ __forceinline__ int column_of(const Job& j, int t) { return __popc(j.mask & ((1u << t) - 1u)); }
@@ -1211,8 +1206,6 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         const int* idx_s = reinterpret_cast<const int*>(smem + OFF_IDX);
         const float* gate_s = reinterpret_cast<const float*>(smem + OFF_GATE);
         const uint32_t* mask_s = reinterpret_cast<const uint32_t*>(smem + OFF_MASK);
-        const int slots_h = p.T * p.K;                          // rows of routed h
-        const size_t h_shared = static_cast<size_t>(slots_h) * p.dff;
         float* out_s = reinterpret_cast<float*>(smem + OFF_OUT);                   // [T][128]
         float* sums = out_s + c.tid;                                               // epilogue: this thread's row
         JobQueue queue;
@@ -1222,38 +1215,8 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         for (int phase = 2; phase <= 3; ++phase) {
             const bool third = phase == 3;
             if (third) {
-                if (MODE == M_BF16) fence_proxy_async_all();    // phase 2 wrote the image
+                fence_proxy_async_all();                        // phase 2 wrote the image of h
                 grid_barrier(p.ctr, 1, p.status, c.abort_flag, c.tid);
-                if (MODE != M_BF16) {
-                    // the image of h, a warp per 128 values; a slot over the
-                    // capacity has none
-                    const int nr = p.dff / 128, ns = p.dffs / 128;
-                    const int routed = slots_h * nr, blocks = routed + p.S * p.T * ns;
-#pragma unroll 1
-                    for (int i = blockIdx.x * CW + c.warp; i < blocks; i += gridDim.x * CW) {
-                        const bool sh = i >= routed;
-                        const int u = sh ? i - routed : i, nb = sh ? ns : nr, row = u / nb, col = (u - row * nb) * 128;
-                        const int k = sh ? p.dffs : p.dff, pieces = pieces_of<MODE>(k);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                            p.h32 + (sh ? h_shared : 0) + static_cast<size_t>(row) * k + col) + c.lane);
-                        if (sh) {
-                            const int s = row / p.T, r8 = rows8<MODE>(p.T);
-                            store_block<MODE>(v, p.hqs + static_cast<size_t>(s * r8) * pieces * 1024,
-                                              p.hss + static_cast<size_t>(s) * pieces * Form<MODE>::SFB, r8, row - s * p.T, col,
-                                              c.lane);
-                            continue;
-                        }
-                        const int t = row / p.K, e = idx_s[t * 16 + row - t * p.K];
-                        const uint32_t m = mask_s[e];
-                        if (!(m >> t & 1u)) continue;
-                        const int base = reinterpret_cast<const int*>(smem + OFF_BASE)[e];
-                        store_block<MODE>(v, p.hq + static_cast<size_t>(base & 0xFFFF) * pieces * 1024,
-                                          p.hs + static_cast<size_t>(base >> 16) * pieces * Form<MODE>::SFB,
-                                          rows8<MODE>(__popc(m)), __popc(m & ((1u << t) - 1u)), col, c.lane);
-                    }
-                    fence_proxy_async_all();
-                    grid_barrier(p.ctr, 2, p.status, c.abort_flag, c.tid);
-                }
                 bar_tokens_ready();
                 ok = ok && *c.abort_flag == 0;
             }
@@ -1285,26 +1248,46 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
                 ok = all_ok(ok);
                 if (!ok || !got) break;
                 const uint32_t tokens = third ? (1u << p.T) - 1u : j.mask;
-                if (!j.ends || !combine(c, j, tokens, out_s) || !in) continue;
+                if (!j.ends || !combine(c, j, tokens, out_s)) continue;
+                if (!third) {
+                    uint8_t* rows = (j.shared ? p.hqs : p.hq) + static_cast<size_t>(j.base8) * pieces_of<MODE>(j.n) * 1024;
+                    uint8_t* scales = (j.shared ? p.hss : p.hs) + static_cast<size_t>(j.rank) * pieces_of<MODE>(j.n) * Form<MODE>::SFB;
+                    const int r8 = rows8<MODE>(__popc(j.mask));
+#pragma unroll 1
+                    for (uint32_t m = tokens; m; m &= m - 1) {
+                        const int t = __ffs(m) - 1;
+                        const float h = silu_fast(sums[t * 128] + bias);
+                        if (MODE == M_BF16) {
+                            // two bytes of row (the token's place) of a piece
+                            if (!in) continue;
+                            const int n = column_of(j, t), at = 2 * row;
+                            uint8_t* dst = rows + (static_cast<size_t>(at >> 7) * r8 + (n >> 3)) * 1024 + (n & 7) * 128 +
+                                           ((((at >> 4) & 7) ^ (n & 7)) << 4) + (at & 15);
+                            *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(h);
+                        } else {
+                            sums[t * 128] = h;
+                        }
+                    }
+                    if (MODE != M_BF16) {
+                        // the tile's rows are 128 columns of h, which a warp per token writes
+                        bar_epilogue();
+                        int i = 0;
+#pragma unroll 1
+                        for (uint32_t m = tokens; m; m &= m - 1, ++i) {
+                            const int t = __ffs(m) - 1;
+                            if ((i & 3) == c.warp)
+                                store_block<MODE>(reinterpret_cast<const float4*>(out_s + t * 128)[c.lane], rows, scales, r8, i,
+                                                  j.row0, c.lane);
+                        }
+                        bar_epilogue();
+                    }
+                    continue;
+                }
+                if (!in) continue;
 #pragma unroll 1
                 for (uint32_t m = tokens; m; m &= m - 1) {
                     const int t = __ffs(m) - 1;
                     float v = sums[t * 128];
-                    if (!third) {
-                        const float h = silu_fast(v + bias);
-                        if (MODE == M_BF16) {
-                            // two bytes of row (the token's place) of a piece
-                            const int n = column_of(j, t), at = 2 * row;
-                            const size_t piece = static_cast<size_t>(j.base8) * pieces_of<MODE>(j.n) +
-                                                 static_cast<size_t>(at >> 7) * rows8<MODE>(__popc(j.mask));
-                            uint8_t* dst = (j.shared ? p.hqs : p.hq) + (piece + (n >> 3)) * 1024 + (n & 7) * 128 +
-                                           ((((at >> 4) & 7) ^ (n & 7)) << 4) + (at & 15);
-                            *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(h);
-                        } else {
-                            p.h32[(j.shared ? h_shared : 0) + static_cast<size_t>(h_row(c, j, t)) * j.n + row] = h;
-                        }
-                        continue;
-                    }
                     const size_t at = static_cast<size_t>(t) * p.d + row;
                     if (p.passthrough) {
 #pragma unroll 1
@@ -1343,7 +1326,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 struct FewLayout {
-    size_t ctr, part, prob, xq, xs, hq, hs, hqs, hss, h32, sums, total;
+    size_t ctr, part, prob, xq, xs, hq, hs, hqs, hss, sums, total;
 };
 
 // blocks: as many as can find work, at most one per SM
@@ -1385,8 +1368,6 @@ FewLayout few_layout_mode(const Dims& dm) {
     FewLayout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) { const size_t o = off; off = align256(off + bytes); return o; };
-    const bool q = MODE != M_BF16;
-    const size_t h = static_cast<size_t>(dm.T) * dm.K * dm.dff + static_cast<size_t>(dm.S) * dm.T * dm.dffs;
     auto pieces = [](int k) { return static_cast<size_t>(pieces_of<MODE>(k)); };
     take(256);                                              // status word
     L.ctr = take((CTR_TILE + SHARES * MAX_BLOCKS) * 4);
@@ -1403,7 +1384,6 @@ FewLayout few_layout_mode(const Dims& dm) {
     L.hs = take(pieces(dm.dff) * reached * Form<MODE>::SFB);
     L.hqs = take(pieces(dm.dffs) * dm.S * rows8<MODE>(dm.T) * 1024);
     L.hss = take(pieces(dm.dffs) * dm.S * Form<MODE>::SFB);
-    L.h32 = take(q ? h * 4 : 0);
     L.sums = take(static_cast<size_t>(SHARES) * MAX_BLOCKS * 2 * dm.T * 128 * 4);
     L.total = off;
     return L;
@@ -1476,7 +1456,6 @@ cudaError_t launch_few(const Dims& dm, const FewArgs& a, void* ws, cudaStream_t 
     p.hs = w + L.hs;
     p.hqs = w + L.hqs;
     p.hss = w + L.hss;
-    p.h32 = reinterpret_cast<float*>(w + L.h32);
     p.sums = reinterpret_cast<float*>(w + L.sums);
     p.alpha = dm.alpha;
     p.T = dm.T;
