@@ -202,6 +202,27 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
+// Loads of weights, which a call reads once: first to leave L2, so that the
+// code, the router and the images stay there.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t v;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(v));
+    return v;
+}
+
+__device__ __forceinline__ void load_weights(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                             uint64_t policy) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%0], [%1, {%3, %4, %5}], [%2], %6;"
+                 :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+                    "l"(policy) : "memory");
+}
+
+__device__ __forceinline__ void load_scales(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                 :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -521,7 +542,7 @@ template <int MODE> __host__ __device__ constexpr int sfa_at(int T) { return sfb
 // back until they are stored, which is when the MMA warp may read them.
 template <int MODE>
 __device__ __forceinline__ bool load_job(const Ctx& c, JobQueue& q, const Job& j, const CUtensorMap* map, const void* scales,
-                                         Ring& ring) {
+                                         uint64_t policy, Ring& ring) {
     constexpr int ELEMS = MODE == M_BF16 ? 64 : 128;        // map elements (bf16, or bytes) per piece
     const int words = j.k / 128;
     const size_t tile = static_cast<size_t>(j.mat) * ((j.n + 127) / 128) + j.row0 / 128;
@@ -555,9 +576,9 @@ __device__ __forceinline__ bool load_job(const Ctx& c, JobQueue& q, const Job& j
             const uint32_t tx = static_cast<uint32_t>(np * PIECE_BYTES) + sfa;
             if (MODE == M_FP8 && s == j.p0) mbar_expect_tx(full, tx);
             else mbar_arrive_expect_tx(full, tx);
-            tma_load_3d(slot, map, full, s * ELEMS, j.row0, j.mat);
-            if (np > 1) tma_load_3d(slot + PIECE_BYTES, map, full, (s + 1) * ELEMS, j.row0, j.mat);
-            if (MODE == M_FP4) bulk_load(slot + sfa_at<MODE>(c.p.T), sc + static_cast<size_t>(s) * 1024, sfa, full);
+            load_weights(slot, map, full, s * ELEMS, j.row0, j.mat, policy);
+            if (np > 1) load_weights(slot + PIECE_BYTES, map, full, (s + 1) * ELEMS, j.row0, j.mat, policy);
+            if (MODE == M_FP4) load_scales(slot + sfa_at<MODE>(c.p.T), sc + static_cast<size_t>(s) * 1024, sfa, full, policy);
         }
         __syncwarp();
         ring.next(c.p.slots);
@@ -1130,6 +1151,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
         }
         __syncthreads();                                        // the experts are selected
         const int n_active = misc[1];
+        const uint64_t policy = evict_first_policy();
         Ring ring;
         JobQueue queue;
         bool ok = *c.abort_flag == 0;
@@ -1150,7 +1172,7 @@ few_tokens_kernel(const __grid_constant__ FewParams p) {
                 while (ok && plan.next(j)) {
                     const void* sc = third ? (j.shared ? p.ws2s : p.w2s) : (j.shared ? p.ws1s : p.w1s);
                     ok = load_job<MODE>(c, queue, j, third ? (j.shared ? &p.ws2 : &p.w2) : (j.shared ? &p.ws1 : &p.w1), sc,
-                                        ring);
+                                        policy, ring);
                 }
                 share = __shfl_sync(0xffffffffu, after, 0);
             }
