@@ -333,8 +333,8 @@ def moe_layer_forward_few(cfg, x, W_r, logit_bias, W1, W1_scales, b1, W2, W2_sca
            "moe_layer_forward_few")
 
 
-def _mxfp4_args(dense, codes, scales, what: str):
-    """(dtype, rows, cols) of a dense matrix and its MXFP4 form, checked against each other."""
+def _mxfp4_args(dense, codes, scales, what: str, stream):
+    """(dtype, rows, cols, stream handle) of a dense matrix and its MXFP4 form, checked against each other."""
     import torch
     dt = dense.dtype
     if dt is not torch.float32 and dt is not torch.bfloat16:
@@ -346,25 +346,30 @@ def _mxfp4_args(dense, codes, scales, what: str):
         raise ValueError(f"{what}: the last dimension ({cols}) must be a multiple of 32")
     if codes.numel() * 2 != n or scales.numel() * 32 != n:
         raise ValueError(f"{what}: codes need (..., cols / 2) and scales (..., cols / 32) elements")
-    dev = dense.device
-    if dev != codes.device or dev != scales.device:
+    dev = dense.get_device()                                   # -1: not on a GPU
+    if dev != codes.get_device() or dev != scales.get_device():
         raise ValueError(f"{what}: all tensors must be on one device")
-    return MOE_F32 if dt is torch.float32 else MOE_BF16, n // cols, cols
+    if dev < 0:
+        raise ValueError("tensor must live on a CUDA device")
+    if not (dense.is_contiguous() and codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("tensor must be contiguous")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: the tensors are on cuda:{dev}, which is not the current device")
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return MOE_F32 if dt is torch.float32 else MOE_BF16, n // cols, cols, st
 
 
 def moe_mxfp4_quantize(x, codes, scales, stream=None):
     """x (..., cols) float32 / bfloat16 into MXFP4: codes uint8 (..., cols / 2), scales uint8 (..., cols / 32)."""
-    dtype, rows, cols = _mxfp4_args(x, codes, scales, "moe_mxfp4_quantize")
-    _on_current_device(x, "moe_mxfp4_quantize")
-    _check(lib().moe_mxfp4_quantize(_p(x), dtype, rows, cols, _p(codes), _p(scales), _stream(stream)),
+    dtype, rows, cols, st = _mxfp4_args(x, codes, scales, "moe_mxfp4_quantize", stream)
+    _check(lib().moe_mxfp4_quantize(x.data_ptr(), dtype, rows, cols, codes.data_ptr(), scales.data_ptr(), st),
            "moe_mxfp4_quantize")
 
 
 def moe_mxfp4_dequantize(codes, scales, out, stream=None):
     """The values of an MXFP4 matrix into out (..., cols) float32 / bfloat16."""
-    dtype, rows, cols = _mxfp4_args(out, codes, scales, "moe_mxfp4_dequantize")
-    _on_current_device(out, "moe_mxfp4_dequantize")
-    _check(lib().moe_mxfp4_dequantize(_p(codes), _p(scales), rows, cols, _p(out), dtype, _stream(stream)),
+    dtype, rows, cols, st = _mxfp4_args(out, codes, scales, "moe_mxfp4_dequantize", stream)
+    _check(lib().moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dtype, st),
            "moe_mxfp4_dequantize")
 
 
