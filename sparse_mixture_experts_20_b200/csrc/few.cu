@@ -51,15 +51,15 @@
 //   warp 8      plans the jobs of the block's shares, and loads weights and
 //               their scales;
 //   warp 9      MMA issue;          warp 10  loads the tokens' images.
-// The weights stream past L2, so at every call the code itself comes from HBM:
-// a phase's first instructions cost as much as its first weights.  The role
-// loops therefore run both phases through the same code (measured: 172 KB of
+// The weights stream past L2, and the code with them unless they are loaded
+// evict-first (306 -> 294 us for sixteen tokens in MXFP4); even so a phase's
+// first instructions cost as much as its first weights.  The role loops therefore run both phases through the same code (measured: 172 KB of
 // code took 10 us to select the experts of one token and 7 us from there to
 // the first weights).
 // Measured (7168 x 2048 experts, 256 of them, top-8 and one shared): MXFP4 one
-// token 49 us, sixteen 304 to 316 (1.62 GB, 5.1 to 5.3 TB/s); FP8 67 and 527 to
-// 538 us (3.04 GB, 5.7 TB/s); bf16, eight tokens, 8 experts of 4096 x 14336,
-// 287 us (1.69 GB, 5.9 TB/s).  The copy rate of the same GPUs is 6.5 TB/s.
+// token 44 us, sixteen 294 to 313 (1.62 GB, 5.2 to 5.5 TB/s); FP8 62 and 514 to
+// 533 us (3.04 GB, 5.7 to 5.9 TB/s); bf16, eight tokens, 8 experts of 4096 x
+// 14336, 293 us (1.69 GB, 5.8 TB/s).  The copy rate of the same GPUs is 6.5 TB/s.
 // Every wait is bounded (common.cuh); after a wait gives up, the warps skip
 // the remaining work but keep meeting at the block's barriers.
 #include <cuda.h>
