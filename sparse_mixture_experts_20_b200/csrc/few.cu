@@ -8,8 +8,8 @@
 // and what a slot of the ring needs of the tokens is one or two bulk copies,
 // because phases 1 and 2 write x and h as the image that the tensor core reads.
 // One block per SM, launched cooperatively; the phases are separated by grid
-// barriers, and since weights do not depend on what the barriers wait for, the
-// ring keeps filling across them:
+// barriers, and since weights do not depend on what the second waits for, the
+// ring keeps filling across it:
 //   1  router logits: (expert, slice of d) dot products in fp32, partial sums
 //      per slice; the image of x;
 //   -- barrier; every block then selects the top-K of all tokens for itself
@@ -53,9 +53,10 @@
 //   warp 9      MMA issue;          warp 10  loads the tokens' images.
 // The weights stream past L2, and the code with them unless they are loaded
 // evict-first (306 -> 294 us for sixteen tokens in MXFP4); even so a phase's
-// first instructions cost as much as its first weights.  The role loops therefore run both phases through the same code (measured: 172 KB of
-// code took 10 us to select the experts of one token and 7 us from there to
-// the first weights).
+// first instructions cost as much as its first weights.  The role loops
+// therefore run both phases through the same code (measured: 172 KB of code
+// took 10 us to select the experts of one token and 7 us from there to the
+// first weights).
 // Measured (7168 x 2048 experts, 256 of them, top-8 and one shared): MXFP4 one
 // token 44 us, sixteen 294 to 313 (1.62 GB, 5.2 to 5.5 TB/s); FP8 62 and 514 to
 // 533 us (3.04 GB, 5.7 to 5.9 TB/s); bf16, eight tokens, 8 experts of 4096 x
@@ -227,6 +228,16 @@ __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ void add_release(uint32_t* p) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" :: "l"(p) : "memory");
+}
+
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t* p) {
+    uint32_t v;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
     uint32_t v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -317,13 +328,14 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
 }
 
 // The general warps of all blocks.  Writes before it are visible to reads
-// (through L2) after it.
+// (through L2) after it: the block's barrier orders them before the release,
+// the acquire before the block's next one (a fence on either side of the
+// atomic took 0.3 us more).
 __device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* status, volatile int* abort_flag, int tid) {
     bar_general();
     if (tid == 0) {
         uint32_t* ctr = ctrs + CTR_BAR + which;
-        __threadfence();
-        atomicAdd(ctr, 1u);
+        add_release(ctr);
         if (*abort_flag) atomicExch(ctrs + CTR_ABORT, 1u);
         uint64_t t0 = 0;
 #pragma unroll 1
@@ -339,7 +351,6 @@ __device__ __noinline__ void grid_barrier(uint32_t* ctrs, int which, int32_t* st
                 }
             }
         }
-        __threadfence();
     }
     bar_general();
 }
@@ -820,13 +831,11 @@ __device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mas
         __stcg(mine + at, out_s[at]);
     }
     int* last_s = reinterpret_cast<int*>(c.smem + OFF_MISC) + 3;
-    __threadfence();
     bar_epilogue();
     if (c.tid == 0) {
         uint32_t* ctr = p.ctr + CTR_TILE + j.share0;
-        const bool last = atomicAdd(ctr, 1u) == static_cast<uint32_t>(parts - 1);
+        const bool last = add_acq_rel(ctr) == static_cast<uint32_t>(parts - 1);
         if (last) *ctr = 0;
-        __threadfence();
         *last_s = last;
     }
     bar_epilogue();
