@@ -366,12 +366,14 @@ __device__ __forceinline__ int column_of(const Job& j, int t) { return __popc(j.
 //
 // Fewer than 64 slots a block: equal shares, none without slots (the join of a
 // further share costs more than it evens out); in phase 2 of whole tiles, which
-// need no join, where that leaves no block more than 1/16 over its share.
-// Else phase 2 has three quarters
-// in a large share per block and the rest, at the end of the sequence, in small
-// ones of 12 slots or more.  Phase 3 has few tiles, and one cut into many
-// shares would be long to add up: there the last eighth of every tile is small
-// shares of its own, of 10 slots or more.
+// need no join, where that leaves no block more than 1/16 over its share (one
+// token: MXFP4 42.8 us, 45.4 without that rule; FP8 60.8 and 63.0).  Else phase
+// 2 has three quarters in a large share per block and the rest, at the end of
+// the sequence, in small ones of 16 slots or more.  Phase 3 has few tiles, and
+// one cut into many shares would be long to add up: there the last eighth of
+// every tile is small shares of its own, of 10 slots or more (sixteen tokens:
+// MXFP4 279 us, FP8 474; with 12 and 10 slots 278 and 478, with 16 and 14 283
+// and 472, with 8 and 7 slower by 14 and 4).
 template <int MODE>
 struct Plan {
     const Ctx& c;
@@ -407,7 +409,7 @@ struct Plan {
                 rest = tiles - shares * most;
                 if (rest) ++shares;
             } else {
-                const int others = lead ? blocks * max(1, min(SMALL, (per - lead) / 12)) : min(blocks, all);
+                const int others = lead ? blocks * max(1, min(SMALL, (per - lead) / 16)) : min(blocks, all);
                 shares = others + (lead ? blocks : 0);
                 each = (all - blocks * lead) / others;
                 extra = all - blocks * lead - each * others;
@@ -843,19 +845,25 @@ __device__ __forceinline__ bool combine(const Ctx& c, const Job& j, uint32_t mas
         bar_epilogue();                                        // the flag may be written again
         return false;
     }
-    // four rows of a token a thread
-#pragma unroll 1
-    for (int i = c.tid; i < p.T * 32; i += EPI) {
-        if (!(mask >> (i / 32) & 1u)) continue;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int x = 0; x < parts; ++x) {
-            const int s = j.share0 + x <= j.share1 ? j.share0 + x : j.small0 + x - (j.share1 - j.share0 + 1);
-            const float4 w = __ldcg(reinterpret_cast<const float4*>(part(s)) + i);
-            v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-        }
-        reinterpret_cast<float4*>(out_s)[i] = v;
+    // four rows of a token a thread, up to four tokens, a few parts at a time
+    float4 v[MAX_T / 4];
+#pragma unroll
+    for (int q = 0; q < MAX_T / 4; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t mine4 = mask >> c.warp;                     // bit 4 q: the q-th token of the warp
+#pragma unroll 4
+    for (int x = 0; x < parts; ++x) {
+        const int s = j.share0 + x <= j.share1 ? j.share0 + x : j.small0 + x - (j.share1 - j.share0 + 1);
+        const float4* src = reinterpret_cast<const float4*>(part(s)) + c.tid;
+#pragma unroll
+        for (int q = 0; q < MAX_T / 4; ++q)
+            if (mine4 >> (4 * q) & 1u) {
+                const float4 w = __ldcg(src + q * EPI);
+                v[q].x += w.x; v[q].y += w.y; v[q].z += w.z; v[q].w += w.w;
+            }
     }
+#pragma unroll
+    for (int q = 0; q < MAX_T / 4; ++q)
+        if (mine4 >> (4 * q) & 1u) reinterpret_cast<float4*>(out_s)[q * EPI + c.tid] = v[q];
     bar_epilogue();
     return true;
 }
