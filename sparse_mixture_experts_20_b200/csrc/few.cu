@@ -58,9 +58,10 @@
 // took 10 us to select the experts of one token and 7 us from there to the
 // first weights).
 // Measured (7168 x 2048 experts, 256 of them, top-8 and one shared): MXFP4 one
-// token 44 us, sixteen 294 to 313 (1.62 GB, 5.2 to 5.5 TB/s); FP8 62 and 514 to
-// 533 us (3.04 GB, 5.7 to 5.9 TB/s); bf16, eight tokens, 8 experts of 4096 x
-// 14336, 293 us (1.69 GB, 5.8 TB/s).  The copy rate of the same GPUs is 6.5 TB/s.
+// token 43 us, sixteen 279 to 298 (1.62 GB, 5.4 to 5.8 TB/s); FP8 61 and 474 to
+// 499 us (3.04 GB, 6.1 to 6.4 TB/s); bf16, eight tokens, 8 experts of 4096 x
+// 14336, 290 to 295 us (1.69 GB, 5.8 TB/s).  The copy rate of the same GPUs is
+// 6.5 TB/s.
 // Every wait is bounded (common.cuh); after a wait gives up, the warps skip
 // the remaining work but keep meeting at the block's barriers.
 #include <cuda.h>
