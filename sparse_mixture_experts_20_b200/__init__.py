@@ -179,6 +179,15 @@ def _stream(stream) -> Optional[int]:
     return getattr(stream, "cuda_stream", stream)
 
 
+def _current(stream):
+    """A context with `stream` (None, a torch stream or a raw handle) as the current one, for the memory that a launch
+    on it writes: what the allocator hands out may still be in use by work queued on the stream it was asked on."""
+    import torch
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)                           # (None: no change)
+
+
 def _on_current_device(t, what: str):
     """The library launches on the current device and its stream: a tensor of another one is refused."""
     import torch
@@ -456,7 +465,7 @@ class MoELayer:
         else:
             self.ws = torch.empty(moe_workspace_size(cfg), dtype=torch.uint8, device=self.device)
             moe_workspace_init(cfg, self.ws)
-        self._few_ws = self.ws if cfg.dtype == MOE_MXFP4 else None
+        self._few_ws = None
         self._cfg_ref = ctypes.byref(cfg)
         out_dt = torch.float32 if cfg.dtype == MOE_F32 else torch.bfloat16
         self.out = torch.empty((cfg.T, cfg.d_model), dtype=out_dt, device=self.device)
@@ -497,14 +506,32 @@ class MoELayer:
         moe_few_workspace_init(self.cfg, ws)
         return ws
 
+    def _first_few(self, stream):
+        """The workspace of the first call of forward_few, cleared on the stream that the call runs on, which waits
+        for the current one (where the layer may just have been built)."""
+        import torch
+        here = torch.cuda.current_stream()
+        captured = torch.cuda.is_current_stream_capturing()
+        with _current(stream):
+            captured = captured or torch.cuda.is_current_stream_capturing()
+            if self.cfg.dtype == MOE_MXFP4 and captured:
+                return self.ws                                  # cleared when the layer was built
+            if captured:
+                raise RuntimeError("forward_few: its first call clears the workspace: make it before capturing")
+            torch.cuda.current_stream().wait_stream(here)
+            self._few_ws = self.ws if self.cfg.dtype == MOE_MXFP4 else self._few_workspace()
+        return self._few_ws
+
     def forward_few(self, x, stream=None):
         """forward(x) in one kernel, for T <= MOE_FEW_MAX_TOKENS.  The first call allocates and clears the
-        workspace (on the current stream): make it before capturing calls into a graph."""
-        if self._few_ws is None:
-            self._few_ws = self._few_workspace()
+        workspace (bf16 and FP8 layers) and orders its stream behind the current one: make it before capturing calls
+        into a graph.  Calls share the workspace and the outputs: those on different streams are yours to order."""
+        ws = self._few_ws
+        if ws is None:
+            ws = self._first_few(stream)
         w = self.w
         tensors = [w.get(k) for k in _FEW_WEIGHTS]
-        tensors += (self.out, self.f, self.P, self.loss, self.topk_idx, self.gates, self.counts, self._few_ws)
+        tensors += (self.out, self.f, self.P, self.loss, self.topk_idx, self.gates, self.counts, ws)
         if x.dtype != self.out.dtype or x.numel() != self.out.numel():
             raise ValueError("forward_few: x must be bfloat16 (T, d_model)")
         _on_current_device(x, "forward_few")

@@ -1,0 +1,107 @@
+"""MoELayer.forward_few around its launch, without a GPU: streams, and what it checks of its tensors."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+import sparse_mixture_experts_20_b200 as M
+
+
+class Stream:
+    def __init__(self, handle, capturing=False):
+        self.cuda_stream, self.capturing, self.waited = handle, capturing, []
+
+    def wait_stream(self, other):
+        self.waited.append(other.cuda_stream)
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """Streams, the workspace's clearing and the launch, as a log of (what, stream handle)."""
+    w = types.SimpleNamespace(now=Stream(0), log=[])
+
+    @contextlib.contextmanager
+    def stream(s):
+        before = w.now
+        w.now = before if s is None else s
+        yield
+        w.now = before
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: w.now)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: w.now.capturing)
+    monkeypatch.setattr(M, "_p", lambda t: None if t is None else t.data_ptr())
+    real = M.lib()
+
+    def launch(*a):
+        w.log.append(("launch", a[-1]))
+        return M.MOE_OK
+
+    fake = types.SimpleNamespace(moe_few_workspace_size=real.moe_few_workspace_size, moe_layer_forward_few=launch)
+    monkeypatch.setattr(M, "lib", lambda: fake)
+    monkeypatch.setattr(M, "moe_few_workspace_init",
+                        lambda cfg, ws, stream=None: w.log.append(("clear", M._stream(stream))))
+    return w
+
+
+def layer(dtype=M.MOE_BF16, **weights):
+    """A layer of T = 4, d = 256, 8 experts of 128 on the CPU, which only the launch above may run."""
+    la = M.MoELayer.__new__(M.MoELayer)
+    la.cfg = M.make_config(T=4, d_model=256, n_routed=8, top_k=2, d_ff=128, dtype=dtype)
+    la._cfg_ref, la.device, la.w, la._few_ws = None, torch.device("cpu"), weights, None
+    la.ws = torch.zeros(256, dtype=torch.uint8)
+    la.out = torch.zeros(4, 256, dtype=torch.bfloat16)
+    la.f = la.P = la.loss = la.topk_idx = la.gates = la.counts = None
+    return la
+
+
+def test_first_call_clears_the_workspace_on_its_own_stream(world):
+    la, side = layer(), Stream(7)
+    la.forward_few(la.out, stream=side)
+    assert world.log == [("clear", 7), ("launch", 7)]
+    assert side.waited == [0]                                   # the layer may just have been built there
+    la.forward_few(la.out)
+    assert world.log[2:] == [("launch", 0)]
+
+
+def test_first_call_on_the_current_stream(world):
+    la = layer()
+    la.forward_few(la.out)
+    assert world.log == [("clear", 0), ("launch", 0)]
+
+
+def test_first_call_on_a_raw_handle(world, monkeypatch):
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: made.append(Stream(h)) or made[-1])
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: Stream(0))
+    la = layer()
+    la.forward_few(la.out, stream=9)
+    assert world.log == [("clear", 9), ("launch", 9)] and made[0].waited == [0]
+    la, world.now, world.log[:] = layer(), Stream(5), []
+    la.forward_few(la.out, stream=0)
+    assert world.log == [("clear", 0), ("launch", 0)]
+
+
+def test_first_call_of_a_four_bit_layer_waits_for_its_building(world):
+    la, side = layer(M.MOE_MXFP4), Stream(7)
+    la.forward_few(la.out, stream=side)
+    assert world.log == [("launch", 7)] and side.waited == [0]
+
+
+@pytest.mark.parametrize("where", ["current", "given"])
+def test_first_call_within_a_capture(world, where):
+    """A bf16 layer's workspace would be cleared by the graph alone; a four-bit layer has its own already."""
+    cap = Stream(7, capturing=True)
+    stream = cap if where == "given" else None
+    world.now = Stream(0) if where == "given" else cap
+    la = layer()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        la.forward_few(la.out, stream=stream)
+    assert world.log == []
+    four = layer(M.MOE_MXFP4)
+    four.forward_few(four.out, stream=stream)
+    assert world.log == [("launch", 7)] and cap.waited == [] and four._few_ws is None
+    la._few_ws = torch.zeros(256, dtype=torch.uint8)
+    la.forward_few(la.out, stream=stream)
+    assert world.log[1:] == [("launch", 7)]
