@@ -598,5 +598,10 @@ class MoELayer:
         cur.wait_stream(s_out)
         return start, end
 
-    def device_status(self, clear: bool = False) -> int:
-        return moe_get_device_status(self.cfg, self.ws, clear=clear)
+    def device_status(self, clear: bool = False, stream=None) -> int:
+        """The status bits of the layer's calls so far, forward_few's included, after synchronising `stream` (the
+        current one by default)."""
+        status = moe_get_device_status(self.cfg, self.ws, stream, clear)
+        if self._few_ws is not None and self._few_ws is not self.ws:
+            status |= moe_get_device_status(self.cfg, self._few_ws, stream, clear)
+        return status

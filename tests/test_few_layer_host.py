@@ -105,3 +105,23 @@ def test_first_call_within_a_capture(world, where):
     la._few_ws = torch.zeros(256, dtype=torch.uint8)
     la.forward_few(la.out, stream=stream)
     assert world.log[1:] == [("launch", 7)]
+
+
+def test_device_status_holds_both_workspaces(monkeypatch):
+    words = {}
+
+    def read(cfg, ws, stream=None, clear=False):
+        v = words[id(ws)]
+        if clear:
+            words[id(ws)] = 0
+        return v
+
+    monkeypatch.setattr(M, "moe_get_device_status", read)
+    la = layer()
+    words[id(la.ws)] = M.MOE_DEV_BAD_ROUTING
+    assert la.device_status() == M.MOE_DEV_BAD_ROUTING          # no few-token call so far
+    la._few_ws = torch.zeros(256, dtype=torch.uint8)
+    words[id(la._few_ws)] = M.MOE_DEV_TIMEOUT
+    assert la.device_status() == M.MOE_DEV_BAD_ROUTING | M.MOE_DEV_TIMEOUT
+    assert la.device_status(clear=True) == M.MOE_DEV_BAD_ROUTING | M.MOE_DEV_TIMEOUT
+    assert la.device_status() == 0

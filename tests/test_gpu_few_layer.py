@@ -57,3 +57,20 @@ def test_first_call_within_a_capture(kind):
         layer.out.zero_()
         graph.replay()
         assert torch.equal(layer.out, want)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_device_status_reports_the_few_token_calls(kind):
+    sh = shape(2, 256, 8, 2, 128)
+    inp, _ = inputs(sh, kind, 5)
+    layer = run(sh, kind, inp)
+    assert layer.device_status() == 0
+    layer._few_ws[:4].view(torch.int32).fill_(M.MOE_DEV_TIMEOUT)          # as a wait that gave up leaves it
+    assert layer.device_status() == M.MOE_DEV_TIMEOUT
+    side = torch.cuda.Stream()
+    assert layer.device_status(clear=True, stream=side) == M.MOE_DEV_TIMEOUT
+    side.synchronize()
+    assert layer.device_status() == 0
+    want = layer.out.clone()
+    layer.forward_few(inp["x"])
+    assert torch.equal(layer.out, want) and layer.device_status() == 0
