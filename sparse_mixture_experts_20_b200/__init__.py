@@ -417,22 +417,45 @@ def moe_mxfp4_get_device_status(shape, ws, stream=None, clear: bool = False) -> 
     return st.value
 
 
+_MXFP4_TYPES: list = []
+
+
 def moe_mxfp4_matmul(shape, a, a_scales, seg_offsets, seg_mat, w, w_scales, bias, y, y_scales, ws, stream=None):
-    """y[r] = act(W_e a[r] + bias_e) over segments of rows, both operands in MXFP4 (shape: make_mxfp4_shape)."""
-    s = shape
-    wb = s.n_mats * s.n * s.k
-    bits = {MOE_F32: 32, MOE_BF16: 16, MOE_MXFP4: 4}.get(s.out_dtype, 0)
-    for name, t, nbytes in (("a", a, s.rows * s.k // 2), ("a_scales", a_scales, s.rows * s.k // 32),
-                            ("seg_offsets", seg_offsets, 4 * (s.n_seg + 1)), ("seg_mat", seg_mat, 4 * s.n_seg),
-                            ("w", w, wb // 2), ("w_scales", w_scales, wb // 32), ("bias", bias, 4 * s.n_mats * s.n),
-                            ("y", y, s.rows * s.n * bits // 8), ("y_scales", y_scales, s.rows * s.n // 32)):
-        if t is not None and t.numel() * t.element_size() < nbytes:
+    """y[r] = act(W_e a[r] + bias_e) over segments of rows, both operands in MXFP4 (shape: make_mxfp4_shape);
+    seg_offsets and seg_mat int32, bias float32, y as the shape's out_dtype says."""
+    import torch
+    rows, n, k, n_mats, n_seg, dtype = shape.rows, shape.n, shape.k, shape.n_mats, shape.n_seg, shape.out_dtype
+    ak, yn, wb = rows * k, rows * n, n_mats * n * k
+    if not _MXFP4_TYPES:                                       # what an operand may be; uint8 and int8 are bytes
+        raw = (torch.uint8, torch.int8)
+        _MXFP4_TYPES.extend(((*raw, torch.float4_e2m1fn_x2), (*raw, torch.float8_e8m0fnu), (torch.int32, *raw),
+                             (torch.float32, *raw), (torch.bfloat16, *raw)))
+    codes, scales, i32, f32, bf16 = _MXFP4_TYPES
+    out, bits = ((f32, 32) if dtype == MOE_F32 else (bf16, 16) if dtype == MOE_BF16 else
+                 (codes, 4 if dtype == MOE_MXFP4 else 0))
+    ptrs, devices = [], set()
+    for name, t, types, nbytes in (
+            ("a", a, codes, ak // 2), ("a_scales", a_scales, scales, ak // 32),
+            ("seg_offsets", seg_offsets, i32, 4 * (n_seg + 1)), ("seg_mat", seg_mat, i32, 4 * n_seg),
+            ("w", w, codes, wb // 2), ("w_scales", w_scales, scales, wb // 32), ("bias", bias, f32, 4 * n_mats * n),
+            ("y", y, out, yn * bits // 8), ("y_scales", y_scales, scales, yn // 32),
+            ("ws", ws, codes, 256)):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype not in types:
+            raise ValueError(f"moe_mxfp4_matmul: {name} is {t.dtype}, not one of {types}")
+        if t.nbytes < nbytes:
             raise ValueError(f"moe_mxfp4_matmul: {name} is smaller than its shape says")
-    if y is not None:
-        _on_current_device(y, "moe_mxfp4_matmul")
-    _check(lib().moe_mxfp4_matmul(ctypes.byref(shape), _p(a), _p(a_scales), _p(seg_offsets), _p(seg_mat), _p(w),
-                                  _p(w_scales), _p(bias), _p(y), _p(y_scales), _p(ws), _stream(stream)),
-           "moe_mxfp4_matmul")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        devices.add(t.get_device())                            # -1: not on a GPU
+        ptrs.append(t.data_ptr())
+    if -1 in devices:
+        raise ValueError("tensor must live on a CUDA device")
+    if devices and devices != {torch._C._cuda_getDevice()}:
+        raise ValueError("moe_mxfp4_matmul: every tensor must be on the current device")
+    _check(lib().moe_mxfp4_matmul(ctypes.byref(shape), *ptrs, _stream(stream)), "moe_mxfp4_matmul")
 
 
 _FEW_WEIGHTS = ("W_r", "logit_bias", "W1", "W1_scales", "b1", "W2", "W2_scales", "b2",
