@@ -17,6 +17,7 @@ whole-layer calls.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -193,6 +194,13 @@ def _on_current_device(t, what: str):
     import torch
     if t.is_cuda and t.device.index != torch._C._cuda_getDevice():
         raise ValueError(f"{what}: the tensors are on {t.device}, which is not the current device")
+
+
+def _typed(t, name: str, what: str, *types):
+    """Refuses a tensor that holds none of `types`; uint8 and int8 stand for the bytes of any."""
+    import torch
+    if t.dtype not in types and t.dtype is not torch.uint8 and t.dtype is not torch.int8:
+        raise ValueError(f"{what}: {name} is {t.dtype}, not {types[0]}")
 
 
 def _check(status: int, where: str):
@@ -509,22 +517,34 @@ class MoELayer:
         return self.out, self.f, self.P, self.loss
 
     def _few_workspace(self):
-        """The few-token layer's workspace; refuses weights smaller than the layer's shape says."""
+        """The few-token layer's workspace; refuses weights of other types, smaller than the layer's shape says, or on
+        another device than the current one.  (A stack's matrices are compared in shape as well: bytes alone would
+        let eight-bit weights pass for twice as many in four.)"""
         import torch
         c = self.cfg
-        bits = {MOE_BF16: 16, MOE_FP8_E4M3_BLOCK: 8, MOE_MXFP4: 4}.get(c.dtype, 0)
-        scale = {MOE_FP8_E4M3_BLOCK: 4, MOE_MXFP4: 512}.get(c.dtype, 0)      # bytes per 128 x 128 block
+        f32 = torch.float32
+        weight, bits = {MOE_BF16: (torch.bfloat16, 16), MOE_FP8_E4M3_BLOCK: (torch.float8_e4m3fn, 8),
+                        MOE_MXFP4: (torch.float4_e2m1fn_x2, 4)}.get(c.dtype, (f32, 0))
         up = lambda n: (n + 127) // 128  # noqa: E731
-        need = {"W_r": 4 * c.n_routed * c.d_model, "logit_bias": 4 * c.n_routed}
+        need = {"W_r": (f32, (c.n_routed, 4 * c.d_model)), "logit_bias": (f32, (4 * c.n_routed,))}
         for p, e, ff in (("W", c.n_routed, c.d_ff), ("Ws", c.n_shared, c.d_ff_shared)):
             for i, rows, cols in ((1, ff, c.d_model), (2, c.d_model, ff)):
-                need[f"{p}{i}"] = e * rows * cols * bits // 8
-                need[f"{p}{i}_scales"] = e * up(rows) * up(cols) * scale
-                need[f"{p.replace('W', 'b')}{i}"] = 4 * e * rows
-        for name, n in need.items():
+                need[f"{p}{i}"] = weight, (e, rows, cols * bits // 8)
+                need[f"{p.replace('W', 'b')}{i}"] = f32, (e, 4 * rows)
+                if c.dtype == MOE_FP8_E4M3_BLOCK:
+                    need[f"{p}{i}_scales"] = f32, (e, up(rows), 4 * up(cols))
+                elif c.dtype == MOE_MXFP4:                     # tiled
+                    need[f"{p}{i}_scales"] = torch.uint8, (e, up(rows), up(cols), 512)
+        for name, (dtype, shape) in need.items():              # shape: the last dimension in bytes
             t = self.w.get(name)
-            if t is not None and t.numel() * t.element_size() < n:
+            if t is None:
+                continue
+            _typed(t, name, "forward_few", dtype)
+            if t.nbytes < math.prod(shape):
                 raise ValueError(f"forward_few: {name} is smaller than its shape says")
+            if len(shape) > 2 and t.dim() == len(shape) and (*t.shape[1:-1], t.shape[-1] * t.element_size()) != shape[1:]:
+                raise ValueError(f"forward_few: {name} has matrices of another shape, {tuple(t.shape[1:])}")
+            _on_current_device(t, "forward_few")
         ws = torch.empty(moe_few_workspace_size(self.cfg), dtype=torch.uint8, device=self.device)
         moe_few_workspace_init(self.cfg, ws)
         return ws

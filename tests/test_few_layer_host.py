@@ -125,3 +125,57 @@ def test_device_status_holds_both_workspaces(monkeypatch):
     assert la.device_status() == M.MOE_DEV_BAD_ROUTING | M.MOE_DEV_TIMEOUT
     assert la.device_status(clear=True) == M.MOE_DEV_BAD_ROUTING | M.MOE_DEV_TIMEOUT
     assert la.device_status() == 0
+
+
+def weights(dtype):
+    """The tensors of layer() as a user holds them (MXFP4 scales tiled)."""
+    E, d, ff = 8, 256, 128
+    w = dict(W_r=torch.zeros(E, d), logit_bias=torch.zeros(E), b1=torch.zeros(E, ff), b2=torch.zeros(E, d))
+    for n, rows, cols in (("W1", ff, d), ("W2", d, ff)):
+        if dtype == M.MOE_BF16:
+            w[n] = torch.zeros(E, rows, cols, dtype=torch.bfloat16)
+        elif dtype == M.MOE_FP8_E4M3_BLOCK:
+            w[n] = torch.zeros(E, rows, cols, dtype=torch.float8_e4m3fn)
+            w[n + "_scales"] = torch.zeros(E, rows // 128, cols // 128)
+        else:
+            w[n] = torch.zeros(E, rows, cols // 2, dtype=torch.uint8)
+            w[n + "_scales"] = torch.zeros(E, rows // 128, cols // 128, 512, dtype=torch.uint8)
+    return w
+
+
+KINDS = [M.MOE_BF16, M.MOE_FP8_E4M3_BLOCK, M.MOE_MXFP4]
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_weights_of_the_layers_types_are_taken(dtype, monkeypatch):
+    monkeypatch.setattr(M, "moe_few_workspace_init", lambda cfg, ws: None)
+    w = weights(dtype)
+    layer(dtype, **w)._few_workspace()
+    layer(dtype, **{k: v.view(torch.uint8) for k, v in w.items()})._few_workspace()          # their bytes
+    layer(dtype, **{k: v.flatten() for k, v in w.items()})._few_workspace()
+    layer(dtype, **{k: torch.cat([v, v]) for k, v in w.items()})._few_workspace()            # more experts than routed
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_weights_of_other_types_are_refused(dtype, monkeypatch):
+    """Larger ones too, which a comparison of sizes would let through."""
+    monkeypatch.setattr(M, "moe_few_workspace_init", lambda cfg, ws: None)
+    w = weights(dtype)
+    for name, t in w.items():
+        for other in (torch.float64, torch.float16, torch.int64, torch.bfloat16 if t.dtype != torch.bfloat16 else torch.float32):
+            with pytest.raises(ValueError, match=f"{name} is torch"):
+                layer(dtype, **{**w, name: torch.zeros(t.shape, dtype=other)})._few_workspace()
+    # the matrices of another form: eight bits for four, twice the rows of half the length
+    for name in ("W1", "W2"):
+        for bad in (torch.cat([w[name], w[name]], -1), w[name].reshape(8, 2 * w[name].shape[1], -1)):
+            with pytest.raises(ValueError, match=f"{name} has matrices of another shape"):
+                layer(dtype, **{**w, name: bad})._few_workspace()
+
+
+def test_weights_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(M, "moe_few_workspace_init", lambda cfg, ws: None)
+    monkeypatch.setattr(M, "_on_current_device", lambda t, what: (_ for _ in ()).throw(ValueError("cuda:1")) if t is there else None)
+    w = weights(M.MOE_BF16)
+    for there in w.values():
+        with pytest.raises(ValueError, match="cuda:1"):
+            layer(**w)._few_workspace()
