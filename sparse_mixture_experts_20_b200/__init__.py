@@ -522,9 +522,10 @@ class MoELayer:
         let eight-bit weights pass for twice as many in four.)"""
         import torch
         c = self.cfg
+        size = moe_few_workspace_size(c)                       # refuses what no weights would make a layer of
         f32 = torch.float32
         weight, bits = {MOE_BF16: (torch.bfloat16, 16), MOE_FP8_E4M3_BLOCK: (torch.float8_e4m3fn, 8),
-                        MOE_MXFP4: (torch.float4_e2m1fn_x2, 4)}.get(c.dtype, (f32, 0))
+                        MOE_MXFP4: (torch.float4_e2m1fn_x2, 4)}[c.dtype]
         up = lambda n: (n + 127) // 128  # noqa: E731
         need = {"W_r": (f32, (c.n_routed, 4 * c.d_model)), "logit_bias": (f32, (4 * c.n_routed,))}
         for p, e, ff in (("W", c.n_routed, c.d_ff), ("Ws", c.n_shared, c.d_ff_shared)):
@@ -545,8 +546,8 @@ class MoELayer:
             if len(shape) > 2 and t.dim() == len(shape) and (*t.shape[1:-1], t.shape[-1] * t.element_size()) != shape[1:]:
                 raise ValueError(f"forward_few: {name} has matrices of another shape, {tuple(t.shape[1:])}")
             _on_current_device(t, "forward_few")
-        ws = torch.empty(moe_few_workspace_size(self.cfg), dtype=torch.uint8, device=self.device)
-        moe_few_workspace_init(self.cfg, ws)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+        moe_few_workspace_init(c, ws)
         return ws
 
     def _first_few(self, stream):

@@ -179,3 +179,15 @@ def test_weights_of_another_device_are_refused(monkeypatch):
     for there in w.values():
         with pytest.raises(ValueError, match="cuda:1"):
             layer(**w)._few_workspace()
+
+
+def test_layers_without_a_few_token_form_say_so():
+    """Before anything is said of their weights: fp32, and more tokens than one kernel takes."""
+    w = {k: v.float() for k, v in weights(M.MOE_BF16).items()}
+    few = layer(M.MOE_F32, **w)
+    many = layer(**weights(M.MOE_BF16))
+    many.cfg.T = 17
+    for la in (few, many):
+        with pytest.raises(M.MoEError) as e:
+            la._few_workspace()
+        assert e.value.status == M.MOE_ERR_UNSUPPORTED
