@@ -996,22 +996,7 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
             if (!in) l[i] = -INFINITY;
             top = fmaxf(top, l[i]);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            l[i] = expf(l[i] - top);
-            sum += l[i];
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (writer) {
-            const float inv = 1.f / sum;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p.prob[t * 256 + 32 * i + c.lane] = l[i] * inv;
-        }
-        float chosen = 0.f, mine = 0.f;
+        float best_l = -INFINITY, mine = 0.f;
 #pragma unroll 1
         for (int k = 0; k < p.K; ++k) {
             uint32_t bk = 0, bi = 0xFFFFu;
@@ -1025,11 +1010,32 @@ __device__ __forceinline__ void select_experts(const Ctx& c) {
             for (int i = 0; i < 8; ++i)
                 if (e == static_cast<uint32_t>(32 * i + c.lane)) { v = l[i]; key[i] = 0; }
             v = __shfl_sync(0xffffffffu, v, e & 31);
-            chosen += v;
+            best_l = fmaxf(best_l, v);
             if (c.lane == k) mine = v;
             if (c.lane == 0) idx_s[t * 16 + k] = static_cast<int>(e);
         }
+        // gates: relative to the largest logit chosen, which a bias on the
+        // selection alone may leave far below the largest of all
+        mine = c.lane < p.K ? expf(mine - best_l) : 0.f;
+        float chosen = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < p.K; ++k) chosen += __shfl_sync(0xffffffffu, mine, k);
         if (c.lane < p.K) gate_s[t * 16 + c.lane] = mine / chosen;
+        if (writer) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                l[i] = expf(l[i] - top);
+                sum += l[i];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p.prob[t * 256 + 32 * i + c.lane] = l[i] * inv;
+        }
         }
     }
     mask_s[c.tid] = 0;

@@ -1,0 +1,56 @@
+"""Gates under a selection-only bias, where the experts chosen lie far below the largest logit: the softmax over the
+chosen ones, as defined, whatever the other logits are."""
+import numpy as np
+import pytest
+import torch
+
+import moe_testlib as TL
+import sparse_mixture_experts_20_b200 as M
+from synthetic import MoEShape
+from test_gpu_few import BF16, FP4, FP8, host_routing, inputs, run
+
+pytestmark = pytest.mark.gpu
+
+
+def far(sh, kind, lead, seed):
+    """Inputs where expert 0's logit is `lead` above zero for every token and a bias of -1e5 keeps it from being
+    chosen; the gates by the definition, and how far an fp32 softmax over the chosen logits may be from them."""
+    inp, _ = inputs(sh, kind, seed)
+    inp["x"][:, 0] = 1.0
+    inp["W_r"][0] = 0.0
+    inp["W_r"][0, 0] = lead
+    inp["logit_bias"] = torch.zeros(sh.n_routed, device="cuda")
+    inp["logit_bias"][0] = -1e5
+    h = host_routing(inp)
+    x, W = h["x"].double().numpy(), h["W_r"].double().numpy()
+    logits = x @ W.T
+    order = np.argsort(-(logits + h["logit_bias"].double().numpy()), axis=1, kind="stable")[:, :sh.top_k]
+    # a logit: at most 16 fp32 steps of the sum of its terms' magnitudes (an fp32 router; a three-plane bf16 one is
+    # nearer); a gate moves by at most twice the largest change of a chosen logit, relative to itself
+    el = 16 * 2.0 ** -24 * np.take_along_axis(np.abs(x) @ np.abs(W).T, order, 1).max(1)
+    top = np.take_along_axis(logits, order, 1)
+    e = np.exp(top - top.max(1, keepdims=True))
+    return inp, logits, order, e / e.sum(1, keepdims=True), 2 * el[:, None] + 2.0 ** -20
+
+
+def check(logits, idx, gates, order, want, tol):
+    """Tokens whose chosen set is clear of ties: the same experts, the same gates."""
+    idx, gates = idx.cpu().numpy(), gates.double().cpu().numpy()
+    assert np.all(np.isfinite(gates))
+    clear = np.all(idx == order, axis=1)
+    assert clear.mean() > 0.9
+    assert np.all(np.abs(gates - want)[clear] <= tol[clear] * want[clear] + 2.0 ** -24)
+    assert np.all(idx != 0)
+
+
+@pytest.mark.parametrize("lead", [20.0, 95.0, 150.0, 3e4])
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_few_tokens(kind, lead):
+    sh = MoEShape("few", 14, 256, 12, 4, 128, bias_mode=1)
+    inp, logits, order, want, tol = far(sh, kind, lead, 31)
+    o = run(sh, kind, inp)
+    check(logits, o.topk_idx, o.gates, order, want, tol)
+    assert bool(torch.isfinite(o.out.float()).all()) and bool((o.out != 0).any(1).all())
+    # the probabilities stay those of all experts
+    p = np.exp(logits - logits.max(1, keepdims=True))
+    assert np.max(np.abs(o.P.double().cpu().numpy() - (p / p.sum(1, keepdims=True)).mean(0))) < 1e-4
