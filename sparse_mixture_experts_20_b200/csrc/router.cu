@@ -133,7 +133,11 @@ __device__ __forceinline__ void select_block(float* lg_raw, int t0, int T, int E
         const float inv = 1.0f / e_sum;
 #pragma unroll
         for (int b = 0; b < EPT; ++b) lg[r][lane + 32 * b] = v[b] * inv;
-        const float es = (lane < K) ? expf(sel_v - vmax) * inv : 0.f;
+        // gates: relative to the largest logit chosen (without a bias on the
+        // selection alone it is vmax), which that bias may leave far below vmax
+        const float cmax = sel_bias == nullptr
+            ? vmax : order_key_value(__reduce_max_sync(0xffffffffu, lane < K ? order_key(sel_v) : 0u));
+        const float es = (lane < K) ? expf(sel_v - cmax) * inv : 0.f;
         float g_sum = es;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) g_sum += __shfl_xor_sync(0xffffffffu, g_sum, off);

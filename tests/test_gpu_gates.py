@@ -54,3 +54,16 @@ def test_few_tokens(kind, lead):
     # the probabilities stay those of all experts
     p = np.exp(logits - logits.max(1, keepdims=True))
     assert np.max(np.abs(o.P.double().cpu().numpy() - (p / p.sum(1, keepdims=True)).mean(0))) < 1e-4
+
+
+# experts: the small router, the generic one (fp32) and the tensor-core one
+@pytest.mark.parametrize("lead", [20.0, 95.0, 150.0, 3e4])
+@pytest.mark.parametrize("dtype,E", [(M.MOE_F32, 8), (BF16, 8), (M.MOE_F32, 96), (BF16, 96), (FP8, 256)])
+def test_ordinary_router(dtype, E, lead):
+    sh = MoEShape("far", 70, 256, E, 4, 128, bias_mode=1, dtype=dtype)
+    inp, logits, order, want, tol = far(sh, dtype, lead, 32)
+    if dtype == M.MOE_F32:
+        inp = {**TL.gpu_inputs(sh, 32), **{k: inp[k] for k in ("W_r", "logit_bias")}, "x": inp["x"].float()}
+    o = TL.run_layer(sh, inp)
+    check(logits, o["topk_idx"], o["gates"], order, want, tol)
+    assert bool(torch.isfinite(o["out"].float()).all())
