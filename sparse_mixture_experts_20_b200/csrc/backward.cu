@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(256) router_grad_warp_kernel(int T, int E, int
             float v = 0.f;
             if (j < E) {
                 v = bal * static_cast<float>(counts[j]);
-                for (int k = 0; k < K; ++k)
-                    if (topk_idx[static_cast<size_t>(t) * K + k] == j) v += (a[static_cast<size_t>(t) * K + k] - common) / S;
+                if (S >= bwd::kGatesDirect)
+                    for (int k = 0; k < K; ++k)
+                        if (topk_idx[static_cast<size_t>(t) * K + k] == j) v += (a[static_cast<size_t>(t) * K + k] - common) / S;
                 lv[i] = lv[i] / z;                   // s_j
             }
             ds[i] = v;
@@ -149,7 +150,12 @@ __global__ void __launch_bounds__(256) router_grad_warp_kernel(int T, int E, int
         for (int i = 0; i < JMAX; ++i) {
             const int j = lane + 32 * i;
             if (j < E) {
-                const float v = lv[i] * (ds[i] - sds);
+                float v = lv[i] * (ds[i] - sds);
+                if (S < bwd::kGatesDirect)
+                    for (int k = 0; k < K; ++k) {
+                        const size_t slot = static_cast<size_t>(t) * K + k;
+                        if (topk_idx[slot] == j) v += gates[slot] * (a[slot] - common);
+                    }
                 dl[static_cast<size_t>(t) * E + j] = v;
                 dl_b[static_cast<size_t>(t) * Epad + j] = __float2bfloat16_rn(v);
             } else if (j < Epad) {

@@ -86,6 +86,13 @@ template <typename XT> struct GateGrad {
     }
 };
 
+// The gates' share of dJ/dl is g_k (a_k - common), which through ds is
+// s_k (a_k - common) / S with S the sum of the chosen s: exact as long as fp32
+// holds the chosen s in full.  Under a selection-only bias they may lie below
+// any fp32 number; under this S the share is added to dl itself, as g_k (a_k -
+// common) of the gates that the forward gave.
+constexpr float kGatesDirect = 7.888609e-31f;      // 2^-100: a chosen s is 2^-26 S or more, or does not matter
+
 // dl[t*E + j]: dJ/dl of token t (softmax of its logits, the gates' and the
 // balance loss's share of ds).
 struct RouterGrad {
@@ -100,7 +107,7 @@ struct RouterGrad {
     MOE_HD float ds_of(size_t t, int j, float S, float common) const {
         float v = bal * static_cast<float>(counts[j]);
         for (int k = 0; k < K; ++k)
-            if (topk_idx[t * K + k] == j) v += (a[t * K + k] - common) / S;
+            if (topk_idx[t * K + k] == j && S >= kGatesDirect) v += (a[t * K + k] - common) / S;
         return v;
     }
     MOE_HD void operator()(size_t t) const {
@@ -119,7 +126,10 @@ struct RouterGrad {
         for (int j = 0; j < E; ++j) sds += (expf(l[j] - m) / z) * ds_of(t, j, S, common);
         for (int j = 0; j < E; ++j) {
             const float s = expf(l[j] - m) / z;
-            dl[t * E + j] = s * (ds_of(t, j, S, common) - sds);
+            float v = s * (ds_of(t, j, S, common) - sds);
+            for (int k = 0; k < K; ++k)
+                if (topk_idx[t * K + k] == j && S < kGatesDirect) v += gates[t * K + k] * (a[t * K + k] - common);
+            dl[t * E + j] = v;
         }
     }
 };

@@ -5,8 +5,10 @@ import pytest
 import torch
 
 import moe_testlib as TL
+import oracle as O
 import sparse_mixture_experts_20_b200 as M
 from synthetic import MoEShape
+from test_gpu_backward import TOL, _grad_buffers
 from test_gpu_few import BF16, FP4, FP8, host_routing, inputs, run
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +69,32 @@ def test_ordinary_router(dtype, E, lead):
     o = TL.run_layer(sh, inp)
     check(logits, o["topk_idx"], o["gates"], order, want, tol)
     assert bool(torch.isfinite(o["out"].float()).all())
+
+
+@pytest.mark.parametrize("lead", [20.0, 60.0, 75.0, 95.0, 150.0])
+@pytest.mark.parametrize("dtype", [M.MOE_F32, BF16])
+def test_backward(dtype, lead):
+    """The gradients through those gates, against the oracle's in fp64."""
+    sh = MoEShape("far", 60, 256, 8, 3, 128, bias_mode=1, dtype=dtype)
+    inp = far(sh, BF16, lead, 33)[0]
+    if dtype == M.MOE_F32:
+        inp = {**TL.gpu_inputs(sh, 33), **{k: inp[k] for k in ("W_r", "logit_bias")}, "x": inp["x"].float()}
+    o = TL.run_stages(sh, inp)
+    dout = torch.randn(inp["x"].shape, generator=torch.Generator().manual_seed(1)).to(inp["x"].dtype)
+    grads = _grad_buffers(sh, inp, "cuda")
+    tensors = {k: inp[k] for k in ("x", "W_r", "W1", "b1", "W2", "b2")}
+    tensors.update({k: o[k] for k in ("logits", "topk_idx", "gates", "counts", "offsets", "slot_row", "row_slot", "x_disp",
+                                      "y")})
+    bws = torch.empty(M.moe_backward_workspace_size(o["cfg"]), dtype=torch.uint8, device="cuda")
+    M.moe_layer_backward(o["cfg"], 1.0, {**tensors, "dout": dout.cuda(), **grads}, bws)
+    host = {k: TL.cpu(v) for k, v in inp.items()}
+    rt = O.route(sh, host, logits=TL.cpu(o["logits"]).double().numpy())
+    assert np.array_equal(rt["idx"], TL.cpu(o["topk_idx"]).numpy()) and not np.any(rt["idx"] == 0)
+    ref = O.layer_backward(sh, host, O.to_f64(dout), lam=1.0, routing=rt)
+    for k, v in grads.items():
+        got, want = TL.cpu(v).double().numpy(), ref["logit_bias" if k == "d_logit_bias" else k[1:]]
+        assert np.isfinite(got).all(), k
+        if np.linalg.norm(want) == 0.0:
+            assert np.all(got == 0.0), k
+        else:
+            assert TL.rel_frob(got, want) < TOL[dtype], k
