@@ -313,9 +313,11 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
  *                             W1 (N_r, d_ff, d_model/2) bytes, W2 (N_r,
  *                             d_model, d_ff/2), with their scales in the order
  *                             of moe_mxfp4_tile_scales; the shared experts
- *                             likewise; x (bf16) and the hidden activation are
- *                             not quantised: they enter as sums of five E2M1
- *                             terms, within amax / 12288 of each 32 columns
+ *                             likewise; x (bf16) and the hidden activation
+ *                             enter as fixed point of about 13 bits per block
+ *                             of 32 columns (sums of five E2M1 terms): a value
+ *                             is held to within max(amax / 12288, 2^-126),
+ *                             amax the largest magnitude of its block
  * In every mode x and out are bf16, biases and W_r fp32; FP8 scales are powers
  * of two.  out may be x itself, and overlaps nothing else.  With MXFP4 weights
  * an infinity in x or in the hidden activation makes NaN of its token's sums.

@@ -36,13 +36,15 @@
 //          memory keeps eight "uniform" sets of scale columns, by exponent
 //          modulo 8, and an MMA names the one it needs;
 //   MXFP4  packed E2M1 with its E8M0 scales (kind::mxf4.block_scale), which lie
-//          tiled in the order that tcgen05.cp reads.  x and h are not
-//          quantised: per 32 columns they are split into five E2M1 planes,
+//          tiled in the order that tcgen05.cp reads.  x and h are
+//          fixed point per 32 columns: split into five E2M1 planes,
 //          each the nearest E2M1 value of what the planes before it left, at
 //          scales s, s/4, s/32, s/256, s/2048.  A plane's remainder is at most
 //          half of the step at its largest magnitude (1, then 1/2 of the next
 //          plane's unit), so the five stand for the value to within s / 4096
-//          <= amax / 12288.  A token is then five columns, which the tensor
+//          <= amax / 12288.  A plane whose scale would be below 2^-127 holds
+//          nothing, which leaves an error of at most 2^-126 (the first plane's
+//          at scale 2^-126).  A token is then five columns, which the tensor
 //          core has to spare.
 //
 // Per block (352 threads):
