@@ -398,7 +398,8 @@ def moe_mxfp4_tile_scales(scales, stream=None):
         raise ValueError("moe_mxfp4_tile_scales: scales are a uint8 stack (n_mats, rows, cols / 32)")
     _on_current_device(scales, "moe_mxfp4_tile_scales")
     n, rows, cols = scales.shape[0], scales.shape[1], scales.shape[2] * 32
-    tiled = torch.empty((n, (rows + 127) // 128, cols // 128, 512), dtype=torch.uint8, device=scales.device)
+    with _current(stream):
+        tiled = torch.empty((n, (rows + 127) // 128, cols // 128, 512), dtype=torch.uint8, device=scales.device)
     _check(lib().moe_mxfp4_tile_scales(_p(scales), n, rows, cols, _p(tiled), _stream(stream)), "moe_mxfp4_tile_scales")
     return tiled
 

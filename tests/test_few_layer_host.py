@@ -191,3 +191,14 @@ def test_layers_without_a_few_token_form_say_so():
         with pytest.raises(M.MoEError) as e:
             la._few_workspace()
         assert e.value.status == M.MOE_ERR_UNSUPPORTED
+
+
+def test_tiled_scales_are_allocated_on_their_launch_stream(world, monkeypatch):
+    """What the allocator gives on another stream may still be in use there."""
+    real, fake = torch.empty, M.lib()
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: world.log.append(("empty", world.now.cuda_stream)) or real(*a, **kw))
+    fake.moe_mxfp4_tile_scales = lambda *a: world.log.append(("launch", a[-1])) or M.MOE_OK
+    scales = torch.zeros(2, 128, 8, dtype=torch.uint8)
+    assert M.moe_mxfp4_tile_scales(scales, stream=Stream(7)).shape == (2, 1, 2, 512)
+    M.moe_mxfp4_tile_scales(scales)
+    assert world.log == [("empty", 7), ("launch", 7), ("empty", 0), ("launch", 0)]

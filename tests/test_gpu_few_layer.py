@@ -74,3 +74,19 @@ def test_device_status_reports_the_few_token_calls(kind):
     want = layer.out.clone()
     layer.forward_few(inp["x"])
     assert torch.equal(layer.out, want) and layer.device_status() == 0
+
+
+def test_tiled_scales_on_a_given_stream():
+    """While the current stream still writes what it has freed."""
+    scales = torch.randint(0, 256, (5, 300, 64), dtype=torch.uint8, generator=torch.Generator().manual_seed(1)).cuda()
+    want = M.moe_mxfp4_tile_scales(scales)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = torch.empty_like(want)
+    torch.cuda._sleep(20_000_000)
+    late.fill_(255)
+    del late
+    got = M.moe_mxfp4_tile_scales(scales, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
