@@ -323,7 +323,8 @@ MOE_EXPORT int moe_layer_forward(const moe_config* cfg, const void* x, const flo
  * an infinity in x or in the hidden activation makes NaN of its token's sums.
  * Errors: MOE_ERR_UNSUPPORTED for MOE_F32, for T > MOE_FEW_MAX_TOKENS, and for
  * d_model or a d_ff that is not a multiple of 64 (bf16) or 128, for d_model
- * above 131072, and for experts reached whose weights number above 2^40.
+ * above 131072, for hidden rows of all experts together above 2^31 - 512, and
+ * for experts reached whose weights number above 2^40.
  * ws: moe_few_workspace_size() bytes, 256-byte aligned, zero-filled once by
  * moe_few_workspace_init before first use and left consistent by every call;
  * calls that overlap on the GPU need one each.  moe_get_device_status reads
@@ -368,7 +369,8 @@ MOE_EXPORT int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales,
  * that moe_layer_forward_few streams: (n_mats, ceil(rows/128), cols/128, 512)
  * bytes, where the four scale bytes of row r of a tile of 128 rows and of 128
  * columns lie at 16 (r mod 32) + 4 (r div 32).  Rows past the end read as 2^0.
- * cols a multiple of 128; pointers 16-byte aligned, not overlapping. */
+ * cols a multiple of 128, rows at most 2^31 - 512; pointers 16-byte aligned, not
+ * overlapping. */
 MOE_EXPORT int moe_mxfp4_tile_scales(const uint8_t* scales, int64_t n_mats, int32_t rows, int32_t cols,
                                      uint8_t* tiled, void* stream);
 
@@ -380,7 +382,8 @@ MOE_EXPORT int moe_mxfp4_tile_scales(const uint8_t* scales, int64_t n_mats, int3
  * fp32, bf16 (round to nearest even), or MXFP4 codes with y_scales, quantised
  * as moe_mxfp4_quantize would the fp32 results: the next product's operand.
  *   a (rows, k/2), a_scales (rows, k/32): 0 <= rows; k a multiple of 128
- *   w (n_mats, n, k/2), w_scales (n_mats, n, k/32): n a multiple of 32
+ *   w (n_mats, n, k/2), w_scales (n_mats, n, k/32): n a multiple of 32; rows, n
+ *     and k at most 2^31 - 512
  *   bias (n_mats, n) fp32 or NULL
  *   seg_offsets (n_seg+1), seg_mat (n_seg) int32 device, 1 <= n_seg <= 256
  *   y (rows, n); y_scales (rows, n/32) with MOE_MXFP4, else NULL

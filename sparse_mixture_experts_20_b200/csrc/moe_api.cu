@@ -19,6 +19,9 @@ int cuda_status(cudaError_t e) {
     return MOE_ERR_CUDA;
 }
 
+// Sizes that 32-bit arithmetic may round up to whole tiles and step past by one.
+constexpr int kMaxExtent = 0x7FFFFFFF - 511;
+
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -166,9 +169,9 @@ int validate_few(const moe_config* cfg, Dims* dm) {
     const int v = validate(&c, dm);
     if (v != MOE_OK) return v;
     if (c.dtype == MOE_F32 || c.T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
-    // the rows of all experts are counted in 32 bits, 16 at a time
+    // the rows of all experts are counted in 32 bits
     const long long rows = static_cast<long long>(dm->E) * dm->dff + static_cast<long long>(dm->S) * dm->dffs;
-    if (rows > (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+    if (rows > kMaxExtent) return MOE_ERR_UNSUPPORTED;
     // A block has one slice of the router (1792 columns), the selection stages
     // the slices' partial logits of at least one token in 207 KB, and the work
     // is counted in slots of 2 x 128 x 64 to 256 weights, in 32 bits.
@@ -619,7 +622,7 @@ int moe_mxfp4_tile_scales(const uint8_t* scales, int64_t n_mats, int32_t rows, i
                           void* stream) {
     NvtxRange nvtx("moe_mxfp4_tile_scales");
     if (n_mats < 0 || rows < 1 || cols < 1) return MOE_ERR_INVALID_ARG;
-    if (cols % 128) return MOE_ERR_UNSUPPORTED;
+    if (cols % 128 || rows > kMaxExtent) return MOE_ERR_UNSUPPORTED;
     const long long per = (static_cast<long long>(rows) + 127) / 128 * cols;     // words of a matrix
     if (n_mats > (1ll << 38) / per) return MOE_ERR_UNSUPPORTED;
     if (n_mats == 0) return MOE_OK;
@@ -632,6 +635,7 @@ static int mxfp4_validate(const moe_mxfp4_shape* s) {
     if (s->activation != MOE_ACT_NONE && s->activation != MOE_ACT_SILU) return MOE_ERR_INVALID_ARG;
     if (s->out_dtype != MOE_F32 && s->out_dtype != MOE_BF16 && s->out_dtype != MOE_MXFP4) return MOE_ERR_INVALID_ARG;
     if (s->n % 32 || s->k % 128 || s->n_mats > 65535 || s->n_seg > 256) return MOE_ERR_UNSUPPORTED;
+    if (s->rows > kMaxExtent || s->n > kMaxExtent || s->k > kMaxExtent) return MOE_ERR_UNSUPPORTED;
     // tiles are counted in 32 bits: at most rows / 128 + n_seg of them per 256 columns
     const long long tiles = (static_cast<long long>(s->rows) / 128 + s->n_seg) * ((s->n + 255) / 256);
     return tiles > (1ll << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
