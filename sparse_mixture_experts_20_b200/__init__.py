@@ -480,7 +480,9 @@ class MoELayer:
     stream and returns (out, f, P, loss); forward_few(x) is the same layer
     through moe_layer_forward_few, for at most MOE_FEW_MAX_TOKENS tokens.  A
     layer of MXFP4 experts has forward_few only; its weights are codes and
-    scales as moe_mxfp4_quantize writes them, the scales tiled here once.
+    scales as moe_mxfp4_quantize writes them, the scales tiled here once.  A
+    layer is of cfg.T tokens; layers of other T over the same experts take this
+    one's w, tiled scales included, and keep no second copy.
     """
 
     def __init__(self, cfg: moe_config, weights: dict, device="cuda"):
@@ -491,7 +493,7 @@ class MoELayer:
         if cfg.dtype == MOE_MXFP4:
             self.w = dict(weights)
             for k in ("W1_scales", "W2_scales", "Ws1_scales", "Ws2_scales"):
-                if weights.get(k) is not None:
+                if weights.get(k) is not None and weights[k].dim() != 4:       # (4: another layer's w has them tiled)
                     self.w[k] = moe_mxfp4_tile_scales(weights[k])
             self.ws = self._few_workspace()
         else:

@@ -90,3 +90,15 @@ def test_tiled_scales_on_a_given_stream():
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP8, FP4])
+def test_layers_of_several_lengths_share_their_weights(kind):
+    sh = shape(6, 256, 8, 2, 256, 1, 128)
+    inp, _ = inputs(sh, kind, 6)
+    first = run(sh, kind, inp)
+    for T in (1, 3, 6):
+        other = M.MoELayer(M.make_config(sh, T=T, dtype=kind), first.w)
+        assert all(other.w[k] is v for k, v in first.w.items())
+        out = other.forward_few(inp["x"][:T])[0]
+        assert torch.equal(out, first.out[:T]) and other.device_status() == 0
