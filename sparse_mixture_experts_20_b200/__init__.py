@@ -184,8 +184,9 @@ def _current(stream):
     """A context with `stream` (None, a torch stream or a raw handle) as the current one, for the memory that a launch
     on it writes: what the allocator hands out may still be in use by work queued on the stream it was asked on."""
     import torch
-    if stream is not None and not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if stream is not None and not hasattr(stream, "wait_stream"):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     return torch.cuda.stream(stream)                           # (None: no change)
 
 
