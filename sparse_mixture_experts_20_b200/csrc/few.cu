@@ -29,7 +29,9 @@
 // who takes a share changes nothing in the sums.
 //
 // Operand forms (products exact, sums in fp32):
-//   bf16   weights, x and h in bf16 (kind::f16);
+//   bf16   weights, x and h in bf16 (kind::f16): h is rounded as the ordinary
+//          layer rounds it, since both operands of an MMA have one type (error
+//          against fp64 2.3e-3; with h in fp32 it would be the output's 1.6e-3);
 //   FP8    e4m3 (kind::mxf8f6f4.block_scale); x and h quantised to e4m3 per 128
 //          columns; all scales are powers of two and go to the tensor core.  A
 //          tile's weight scale is one number for 128 columns of K: tensor

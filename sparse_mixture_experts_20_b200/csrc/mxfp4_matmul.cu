@@ -31,13 +31,16 @@
 //               512 bytes per 128 rows and 128 elements of K, row r's four
 //               bytes at 16 (r mod 32) + 4 (r div 32).  Their scattered reads
 //               are later than the TMA's: with a ring twice as long as the
-//               codes' they run ahead of them (4096-token experts 1041 -> 952 us);
+//               codes' they run ahead of them (4096-token experts 1041 -> 952 us
+//               in runs of their own);
 //   warp 14     relay: makes the proxy fence for a slot of scales, which in a
 //               loader would wait for the reads it has in flight.
 // Measured: 8191 rows x 14336 x 4096 in 273 us alone, 3.5 PFLOP/s (its MMAs
 // in flight 43 % of the cycles), 379 in a row of launches at the power limit;
-// 1024 rows of 256 experts, both layers, 405 to 436 us, 6.0 to 5.6 TB/s of
-// weights.  CTA pairs (256 x 256 tiles) were 1.2 to 1.5 times slower.
+// 1024 rows of 256 experts, both layers, 392 to 436 us, 6.2 to 5.6 TB/s of
+// weights; 32768 rows, 952 us in a run of its own and 1055 to 1142 in a row of
+// launches, at the power limit.  CTA pairs (256 x 256 tiles) were 1.2 to 1.5
+// times slower.
 // Every wait is bounded (common.cuh).
 #include "ffn_common.cuh"
 #include "mxfp4.cuh"
