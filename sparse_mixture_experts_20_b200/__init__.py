@@ -484,6 +484,9 @@ class MoELayer:
     scales as moe_mxfp4_quantize writes them, the scales tiled here once.  A
     layer is of cfg.T tokens; layers of other T over the same experts take this
     one's w, tiled scales included, and keep no second copy.
+    Building clears the workspace (and tiles scales) on the current stream:
+    calls on other streams are ordered behind it by the caller, except that the
+    first of forward_few waits by itself.
     """
 
     def __init__(self, cfg: moe_config, weights: dict, device="cuda"):
